@@ -337,6 +337,102 @@ lsa_status lsa_indexer_train_step(const void *h, const void *W_dq, const void *W
                                   void *workspace, size_t workspace_bytes, lsa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Core attention, part 1 -- the window cache: the keys and values of the tokens that are never
+ * offloaded (hyper.ai summary, "Method": the sliding window's KV), in pages.
+ *     token i of sequence b (rows q_offsets[b] + i of q, k, v) stands at p = cache_len[b] + i,
+ *     in slot p % page_size of page page_table[b][p / page_size];
+ *     the first rot_dim dimensions of every query and key head are rotated in pairs (x1, x2):
+ *         y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a,  a = p inv_freq[j], j < rot_dim / 2,
+ *     pairs (j, j + rot_dim / 2), or neighbours (2j, 2j + 1) with interleaved != 0.
+ *   q, k, v      [N][H_q | H_kv][D] dt; q_stride, k_stride, v_stride elements from one token to the
+ *                next (heads of a token contiguous: slices of one fused projection work directly);
+ *                q nullable together with q_out
+ *   dt, cdt      LSA_F32 into an LSA_F32 cache; LSA_BF16 into LSA_BF16 or LSA_FP8_E4M3
+ *   q_offsets    [B+1] int64 device: tokens of each sequence; q_offsets[B] <= N (rows of q_out
+ *                behind it are left as they are, as is every slot that no token falls on)
+ *   cache_len    [B] int32 device: tokens of each sequence before this call
+ *   page_table   [B][max_pages] int32 device; pages that no new token falls on are not looked at
+ *   inv_freq     [rot_dim / 2] fp32 device (NULL with rot_dim = 0); angles are formed in fp64
+ *   k_cache, v_cache  [n_pages][H_kv][page_size][D] cdt, 16-byte aligned
+ *   k_scale, v_scale  [n_pages][H_kv] fp32, for LSA_FP8_E4M3 only: value = scale * decode(code).
+ *                The call writes powers of two: the least 2^e >= 2^-64 with amax <= 448 * 2^e over the
+ *                page's new tokens of the head, or the scale that the page has where that is larger
+ *                and the page already holds tokens; when the scale grows, the earlier codes are
+ *                rounded again to it.  Infinite values saturate, NaN is stored as NaN.
+ *   q_out        [N][H_q][D] dt: the rotated queries (may be q itself when q_stride = H_q * D)
+ * D in {32, 64, 128}, page_size in {16, 32, 64, 128}, rot_dim a multiple of 16 up to D.  One launch,
+ * no workspace.  A page that two new tokens' sequences share is written by both, in no fixed order.
+ * Bad lengths, offsets and pages are skipped and flagged in the device error word.
+ * ---------------------------------------------------------------------------------------- */
+lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, lsa_dtype dt,
+                         const int64_t *q_offsets, int64_t N, int B, const int32_t *cache_len,
+                         const int32_t *page_table, int max_pages,
+                         const float *inv_freq, int rot_dim, int interleaved,
+                         int H_q, int H_kv, int D, int page_size, int64_t n_pages,
+                         void *k_cache, void *v_cache, lsa_dtype cdt, float *k_scale, float *v_scale,
+                         void *q_out, lsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Core attention, part 2 -- attention over the window cache with a sliding window and first tokens
+ * that stay visible.  Query token i of sequence b stands at p = cache_len[b] + i (as in
+ * lsa_kv_append, whose cache_len and q_offsets serve both calls) and sees the keys
+ *     j <= p  with  window = 0, or j > p - window, or j < n_sink;
+ * query head hq reads key/value head hq / (H_q / H_kv):
+ *     x_j = softmax_scale q . k_j,   out = sum_j exp(x_j) v_j / sum_j exp(x_j),
+ *     lse = log sum_j exp(x_j);   a query that sees no key gets out = 0, lse = -inf.
+ *   q            [N][H_q][D] dt, q_stride elements from one token to the next
+ *   dt, cdt      LSA_F32 with an LSA_F32 cache; LSA_BF16 with LSA_BF16 or LSA_FP8_E4M3 (k_scale,
+ *                v_scale [n_pages][H_kv]: 0, or in [2^-100, 2^120])
+ *   page_table   pages that no query sees are not looked at (they may have been given back)
+ *   out          [N][H_q][D] dt; lse_out [N][H_q] fp32 (nullable)
+ * Products and sums are fp32; probabilities enter the value product in bf16 (f16 for E4M3 caches).
+ * Limits as lsa_kv_append; H_q a multiple of H_kv; max_pages * page_size below 2^31.  Bad lengths,
+ * offsets, pages and scales are flagged, their keys left out.
+ * Workspace: lsa_window_attention_workspace_size (partial results of keys split over CTAs).
+ * ---------------------------------------------------------------------------------------- */
+size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D);
+
+lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt,
+                                const int64_t *q_offsets, int64_t N, int B, const int32_t *cache_len,
+                                const int32_t *page_table, int max_pages,
+                                int H_q, int H_kv, int D, int page_size, int64_t n_pages,
+                                const void *k_cache, const void *v_cache, lsa_dtype cdt,
+                                const float *k_scale, const float *v_scale,
+                                int window, int n_sink, float softmax_scale,
+                                void *out, float *lse_out,
+                                void *workspace, size_t workspace_bytes, lsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Core attention of a decode step -- one softmax over the query's Top-k entries and its window
+ * (hyper.ai summary, "Method": the Top-k entries concatenated with the sliding window's KV).  The
+ * keys of lsa_window_attention, and for each e = topk_idx[n][.] >= 0 the row of entry e of the
+ * sequence that token n belongs to:
+ *     hot_kv[off_b + j] where idx[off_b + j] = e (j < count[b]), for e < S_b;
+ *     win_kv[b][e - S_b] for an entry compressed during the window, S_b <= e < S_b + W.
+ * A row is [2][H_kv][D] in dt: the entry's keys, then its values.  An entry listed twice counts
+ * twice; an entry that is in neither place is flagged and left out.
+ *   topk_idx     [N][k] int32, as lsa_lightning_topk_step writes it for one token per sequence (-1: none)
+ *   idx, count, seq_offsets, total_S, hot_kv   as lsa_fetch_gather leaves them; row_bytes =
+ *                2 * H_kv * D * sizeof(dt), rows 16-byte aligned
+ *   win_kv       [B][W][row_bytes] (nullable with W = 0)
+ * dt = cdt: LSA_F32 or LSA_BF16.  The rest as lsa_window_attention.
+ * ---------------------------------------------------------------------------------------- */
+size_t lsa_core_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D, int k);
+
+lsa_status lsa_core_attention(const void *q, int64_t q_stride, lsa_dtype dt,
+                              const int64_t *q_offsets, int64_t N, int B, const int32_t *cache_len,
+                              const int32_t *page_table, int max_pages,
+                              int H_q, int H_kv, int D, int page_size, int64_t n_pages,
+                              const void *k_cache, const void *v_cache,
+                              int window, int n_sink, float softmax_scale,
+                              const int32_t *topk_idx, int k, const int32_t *idx, const int32_t *count,
+                              const int64_t *seq_offsets, int64_t total_S,
+                              const void *hot_kv, size_t row_bytes, const void *win_kv, int W,
+                              void *out, float *lse_out,
+                              void *workspace, size_t workspace_bytes, lsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * Cold-pool helpers: page-locked host memory mapped into every device's address space
  * (cudaHostAlloc with the Mapped and Portable flags).  The pointer is valid on the host and,
  * unchanged, in kernels.  lsa_pool_free releases memory from lsa_pool_alloc only.

@@ -1,0 +1,360 @@
+// Appending keys and values to a paged cache, with the position rotation applied on the way.
+//
+// Token i of sequence b stands at position p = cache_len[b] + i, in slot p % page of page
+// page_table[b][p / page]; the cache is [n_pages][H][page][D].  The first R dimensions of every query
+// and key head are rotated in pairs (x1, x2), j < R / 2, by the angle a = p inv_freq[j]:
+//     y1 = x1 cos a - x2 sin a,   y2 = x2 cos a + x1 sin a
+// (pairs (j, j + R/2), or neighbours (2j, 2j + 1)).  At positions of a million an fp32 product would
+// leave the angle off by up to 0.06: the turns p inv_freq / 2 pi are formed and reduced to [-1/2, 1/2] in
+// fp64, then rounded once to fp32 (the angle is off by at most 2e-7) for sincospif.  The rotated value
+// is rounded once to the cache's type.
+//
+// An E4M3 cache holds one scale per page, head and tensor.  The scale is a power of two, so moving the
+// page's earlier codes to a larger scale is exact except where they become subnormal; the least one
+// with amax <= 448 scale leaves the largest value in the top two binades of E4M3.  A page that already
+// holds tokens keeps its scale unless the new ones need a larger one.
+//
+// The work is one pass over the data and bound by HBM; a unit is 16 elements of a row (both partners of
+// eight pairs), so no thread needs another's values.  Rows that are stored as they are read go by token
+// (k_kv_append_rows); an E4M3 page and head is one CTA (its scale needs all its new values, held in
+// registers, and nobody else touches the page).  Both kinds of CTA share one launch.
+#pragma once
+#include "common.cuh"
+
+namespace lsa {
+
+struct AppendArgs {
+    const void *q, *k, *v;          // [N][heads][D], rows of a token contiguous
+    int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+    const int64_t *q_offsets;       // [B + 1]
+    const int32_t *cache_len;       // [B]
+    const int32_t *page_table;      // [B][max_pages]
+    const float *inv_freq;          // [rot / 2]
+    void *q_out, *k_cache, *v_cache;
+    float *k_scale, *v_scale;       // [n_pages][H], E4M3 only
+    int64_t N, n_pages;
+    int B, max_pages, Hq, H, D, page, rot, interleaved;
+    int row_ctas_per_token;         // CTAs of one token's rows
+    int64_t row_ctas;               // CTAs [0, row_ctas) go by token, the others by page
+};
+
+// Elements of unit u of a row: two runs of 8 starting at a and b.
+__device__ __forceinline__ void unit_runs(const AppendArgs &A, int u, int &a, int &b)
+{
+    if (!A.interleaved && u < A.rot / 16) {
+        a = u * 8;
+        b = a + A.rot / 2;
+    } else {
+        a = u * 16;
+        b = a + 8;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void load_run8(const void *row, int64_t e, float (&x)[8])
+{
+    if constexpr (DT == DT_F32) {
+        const float4 a = __ldg((const float4 *)((const float *)row + e));
+        const float4 b = __ldg((const float4 *)((const float *)row + e) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 w = __ldg((const uint4 *)((const __nv_bfloat16 *)row + e));
+        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            x[2 * i] = __uint_as_float(r[i] << 16);
+            x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_run8(void *row, int64_t e, const float (&x)[8])
+{
+    if constexpr (DT == DT_F32) {
+        float4 *p = (float4 *)((float *)row + e);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        *(uint4 *)((__nv_bfloat16 *)row + e) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
+// cos and sin of pos * inv_freq.
+__device__ __forceinline__ void turn(int64_t pos, float inv_freq, float &c, float &s)
+{
+    double t = (double)pos * (double)inv_freq * 0.15915494309189533577;  // 1 / 2 pi
+    t -= rint(t);
+    sincospif((float)(t + t), &s, &c);
+}
+
+// Rotate the eight pairs of a unit: x runs a and b (halves: a[i] with b[i]; neighbours: within a, within b).
+__device__ __forceinline__ void rotate_unit(bool interleaved, const float (&c)[8], const float (&s)[8], float (&a)[8],
+                                            float (&b)[8])
+{
+    if (!interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float x1 = a[i], x2 = b[i];
+            a[i] = x1 * c[i] - x2 * s[i];
+            b[i] = x2 * c[i] + x1 * s[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float x1 = a[2 * i], x2 = a[2 * i + 1], z1 = b[2 * i], z2 = b[2 * i + 1];
+            a[2 * i] = x1 * c[i] - x2 * s[i];
+            a[2 * i + 1] = x2 * c[i] + x1 * s[i];
+            b[2 * i] = z1 * c[4 + i] - z2 * s[4 + i];
+            b[2 * i + 1] = z2 * c[4 + i] + z1 * s[4 + i];
+        }
+    }
+}
+
+// The sequence of token n (B: none).  Every thread of the block calls it; one round of loads.
+__device__ __forceinline__ int block_seq_of_token(const int64_t *q_offsets, int B, int64_t N, int64_t n, int *slot)
+{
+    if (threadIdx.x == 0) *slot = B;
+    __syncthreads();
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+        const int64_t lo = __ldg(q_offsets + b), hi = __ldg(q_offsets + b + 1);
+        if (lo < 0 || hi < lo || hi > N) flag(ERRF_OFFSETS);
+        else if (lo <= n && n < hi) atomicMin(slot, b);
+    }
+    __syncthreads();
+    return *slot;
+}
+
+// Page of position pos of sequence b, or -1 (flagged) where the table has none.
+__device__ __forceinline__ int32_t page_of(const int32_t *page_table, int max_pages, int64_t n_pages, int b, int64_t pi)
+{
+    if (pi < 0 || pi >= max_pages) {
+        flag(ERRF_COUNT);
+        return -1;
+    }
+    const int32_t p = __ldg(page_table + (int64_t)b * max_pages + pi);
+    if (p < 0 || p >= n_pages) {
+        flag(ERRF_PAGE);
+        return -1;
+    }
+    return p;
+}
+
+// Rows that are stored in the type they are read in (queries; keys and values of an fp32 or bf16 cache).
+template <int DT, bool KV>
+__device__ __forceinline__ void append_rows(const AppendArgs &A, float2 *cs, int *slot)
+{
+    const int64_t n = blockIdx.x / A.row_ctas_per_token;
+    const int part = blockIdx.x % A.row_ctas_per_token;
+    const int nq = A.q ? A.Hq : 0;
+    const int rows = nq + (KV ? 2 * A.H : 0);
+    const int upr = A.D / 16, units = rows * upr;
+    const int b = block_seq_of_token(A.q_offsets, A.B, A.N, n, slot);
+    if (b >= A.B) return;  // a row behind the last sequence: left as it is
+    const int64_t len = __ldg(A.cache_len + b);
+    if (len < 0) {
+        if (threadIdx.x == 0) flag(ERRF_COUNT);
+        return;
+    }
+    const int64_t pos = len + (n - __ldg(A.q_offsets + b));
+    for (int j = threadIdx.x; j < A.rot / 2; j += blockDim.x) {
+        float c, s;
+        turn(pos, __ldg(A.inv_freq + j), c, s);
+        cs[j] = make_float2(c, s);
+    }
+    int32_t page = -1;
+    if (KV) page = page_of(A.page_table, A.max_pages, A.n_pages, b, pos / A.page);
+    __syncthreads();
+    for (int i = part * blockDim.x + threadIdx.x; i < units; i += A.row_ctas_per_token * blockDim.x) {
+        const int row = i / upr, u = i % upr;
+        const void *src;
+        void *dst;
+        int64_t se, de;
+        bool rot = u < A.rot / 16;
+        if (row < nq) {
+            src = A.q; se = n * A.q_stride + (int64_t)row * A.D;
+            dst = A.q_out; de = (n * A.Hq + row) * A.D;
+        } else {
+            const bool is_v = row >= nq + A.H;
+            const int h = row - nq - (is_v ? A.H : 0);
+            src = is_v ? A.v : A.k;
+            se = n * (is_v ? A.v_stride : A.k_stride) + (int64_t)h * A.D;
+            dst = is_v ? A.v_cache : A.k_cache;
+            de = (((int64_t)page * A.H + h) * A.page + pos % A.page) * A.D;
+            rot = rot && !is_v;
+            if (page < 0) continue;
+        }
+        int ra, rb;
+        if (rot) unit_runs(A, u, ra, rb);
+        else { ra = u * 16; rb = ra + 8; }
+        float xa[8], xb[8];
+        load_run8<DT>(src, se + ra, xa);
+        load_run8<DT>(src, se + rb, xb);
+        if (rot) {
+            float c[8], s[8];
+#pragma unroll
+            for (int t = 0; t < 8; t++) {
+                const float2 v = cs[u * 8 + t];
+                c[t] = v.x;
+                s[t] = v.y;
+            }
+            rotate_unit(A.interleaved, c, s, xa, xb);
+        }
+        store_run8<DT>(dst, de + ra, xa);
+        store_run8<DT>(dst, de + rb, xb);
+    }
+}
+
+// Power of two 2^e, least with amax <= 448 * 2^e (448 = 1.75 * 2^8), at least 2^-64; amax finite, >= 0.
+__device__ __forceinline__ float e4m3_scale(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)((e < -64 ? -64 : e) + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+constexpr int APPEND_PAGE_THREADS = 256;
+constexpr int APPEND_PAGE_UNITS = 4;  // units of a thread: 128 tokens x 128 dimensions / 16 / 256
+
+// One page and head of an E4M3 cache, keys or values.
+template <int DT>
+__device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, int *slot, float *red)
+{
+    const int tensor = (int)(job % 2);
+    const int h = (int)((job / 2) % A.H);
+    const int64_t pj = job / 2 / A.H;
+    // Page jobs of sequence b are numbered from off_b / page + 2b: a sequence of n tokens touches at
+    // most n / page + 2 pages, so the ranges do not meet.  Largest b whose range starts at or before pj.
+    if (threadIdx.x == 0) *slot = -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < A.B; b += blockDim.x) {
+        const int64_t lo = __ldg(A.q_offsets + b), hi = __ldg(A.q_offsets + b + 1);
+        if (lo < 0 || hi < lo || hi > A.N) flag(ERRF_OFFSETS);
+        else if (lo / A.page + 2 * (int64_t)b <= pj) atomicMax(slot, b);
+    }
+    __syncthreads();
+    const int b = *slot;
+    if (b < 0) return;
+    const int64_t off = __ldg(A.q_offsets + b);
+    const int64_t n = __ldg(A.q_offsets + b + 1) - off;
+    const int64_t len = __ldg(A.cache_len + b);
+    if (n == 0) return;
+    if (len < 0) {
+        if (threadIdx.x == 0) flag(ERRF_COUNT);
+        return;
+    }
+    const int64_t pi = len / A.page + (pj - (off / A.page + 2 * (int64_t)b));
+    const int64_t first = max(len, pi * A.page), last = min(len + n, (pi + 1) * A.page);
+    if (first >= last) return;
+    const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, pi);
+    if (page < 0) return;
+    const void *src = tensor ? A.v : A.k;
+    const int64_t stride = tensor ? A.v_stride : A.k_stride;
+    uint8_t *cache = (uint8_t *)(tensor ? A.v_cache : A.k_cache) + ((int64_t)page * A.H + h) * A.page * A.D;
+    float *scale = (tensor ? A.v_scale : A.k_scale) + (int64_t)page * A.H + h;
+    const int held = (int)(first - pi * A.page);  // tokens that the page holds already
+    const int upr = A.D / 16, units = (int)(last - first) * upr;
+
+    float x[APPEND_PAGE_UNITS][16];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < APPEND_PAGE_UNITS; k++) {
+        const int i = threadIdx.x + k * APPEND_PAGE_THREADS;
+        if (i < units) {
+            const int64_t pos = first + i / upr;
+            const int u = i % upr;
+            int ra, rb;
+            const bool rot = !tensor && u < A.rot / 16;
+            if (rot) unit_runs(A, u, ra, rb);
+            else { ra = u * 16; rb = ra + 8; }
+            const int64_t se = (off + pos - len) * stride + (int64_t)h * A.D;
+            float xa[8], xb[8];
+            load_run8<DT>(src, se + ra, xa);
+            load_run8<DT>(src, se + rb, xb);
+            if (rot) {
+                float c[8], s[8];
+#pragma unroll
+                for (int t = 0; t < 8; t++) turn(pos, __ldg(A.inv_freq + u * 8 + t), c[t], s[t]);
+                rotate_unit(A.interleaved, c, s, xa, xb);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; t++) {
+                x[k][t] = xa[t];
+                x[k][8 + t] = xb[t];
+                // (infinities and NaN set no scale: the former saturate, the latter are stored as NaN)
+                const float ua = fabsf(xa[t]), ub = fabsf(xb[t]);
+                if (ua <= 3.4028235e38f) amax = fmaxf(amax, ua);
+                if (ub <= 3.4028235e38f) amax = fmaxf(amax, ub);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    const float before = held ? *scale : 0.f;
+    __syncthreads();  // (also: every thread has read the old scale)
+#pragma unroll
+    for (int wi = 0; wi < APPEND_PAGE_THREADS / 32; wi++) amax = fmaxf(amax, red[wi]);
+    float now = e4m3_scale(amax);
+    if (held) {
+        if (!(before >= 0.f) || before > 3.4028235e38f) {
+            if (threadIdx.x == 0) flag(ERRF_SCALE);
+        } else if (before >= now) {
+            now = before;
+        } else {
+            const float f = before / now;
+            for (int i = threadIdx.x; i < held * upr; i += APPEND_PAGE_THREADS) {
+                uint4 w = *(uint4 *)(cache + (int64_t)i * 16);
+                uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int t = 0; t < 4; t++)
+                    r[t] = pack_e4m3x4(f * e4m3_to_float(r[t] & 255), f * e4m3_to_float((r[t] >> 8) & 255),
+                                       f * e4m3_to_float((r[t] >> 16) & 255), f * e4m3_to_float(r[t] >> 24));
+                *(uint4 *)(cache + (int64_t)i * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+        }
+    }
+    if (threadIdx.x == 0) *scale = now;
+#pragma unroll
+    for (int k = 0; k < APPEND_PAGE_UNITS; k++) {
+        const int i = threadIdx.x + k * APPEND_PAGE_THREADS;
+        if (i < units) {
+            const int u = i % upr;
+            int ra, rb;
+            if (!tensor && u < A.rot / 16) unit_runs(A, u, ra, rb);
+            else { ra = u * 16; rb = ra + 8; }
+            uint8_t *row = cache + (int64_t)(held + i / upr) * A.D;
+            // (a quotient, not a product with 1 / now: a scale kept from the page's own history need not be a power of two)
+            *(uint2 *)(row + ra) = make_uint2(pack_e4m3x4(x[k][0] / now, x[k][1] / now, x[k][2] / now, x[k][3] / now),
+                                              pack_e4m3x4(x[k][4] / now, x[k][5] / now, x[k][6] / now, x[k][7] / now));
+            *(uint2 *)(row + rb) = make_uint2(pack_e4m3x4(x[k][8] / now, x[k][9] / now, x[k][10] / now, x[k][11] / now),
+                                              pack_e4m3x4(x[k][12] / now, x[k][13] / now, x[k][14] / now, x[k][15] / now));
+        }
+    }
+}
+
+template <int DT, bool FP8>
+__global__ void __launch_bounds__(APPEND_PAGE_THREADS) k_kv_append(const AppendArgs A)
+{
+    extern __shared__ float2 cs[];  // [rot / 2] cos, sin of the token
+    __shared__ int slot;
+    __shared__ float red[APPEND_PAGE_THREADS / 32];
+    if (!FP8 || (int64_t)blockIdx.x < A.row_ctas) append_rows<DT, !FP8>(A, cs, &slot);
+    else if constexpr (FP8) append_page<DT>(A, (int64_t)blockIdx.x - A.row_ctas, &slot, red);
+}
+
+}  // namespace lsa

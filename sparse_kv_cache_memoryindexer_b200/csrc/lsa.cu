@@ -22,6 +22,8 @@
 #include "train_tc.cuh"
 #include "step_select.cuh"
 #include "topk.cuh"
+#include "kv_append.cuh"
+#include "attn.cuh"
 #include "selftest.cuh"
 
 using namespace lsa;
@@ -231,10 +233,10 @@ lsa_status lsa_check_device(lsa_stream_t stream)
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_err_word, &zero, sizeof(zero));
     if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "clearing the device error word: %s", cudaGetErrorString(e));
-    return fail(LSA_ERR_DEVICE_CHECK, "device check flags 0x%x:%s%s%s%s%s", word,
+    return fail(LSA_ERR_DEVICE_CHECK, "device check flags 0x%x:%s%s%s%s%s%s", word,
                 (word & ERRF_OFFSETS) ? " bad-seq-offsets" : "", (word & ERRF_INDEX) ? " index-out-of-range" : "",
                 (word & ERRF_COUNT) ? " count-out-of-range" : "", (word & ERRF_SCALE) ? " bad-key-scale" : "",
-                (word & ERRF_TIMEOUT) ? " pipeline-wait-timeout" : "");
+                (word & ERRF_TIMEOUT) ? " pipeline-wait-timeout" : "", (word & ERRF_PAGE) ? " bad-page" : "");
 }
 
 lsa_status lsa_selftest_wait_timeout(int32_t *status_out, lsa_stream_t stream)
@@ -1053,6 +1055,191 @@ lsa_status lsa_memindex_score_select_static(const void *q, const float *w, const
     return lsa_memindex_score_select(q, w, K, k_scale, kdt, seq_offsets, total_S, L, B, n_h, d_I, threshold,
                                      scores_out, mask_out, idx_out, count_out, scratch,
                                      (size_t)LSA_STATIC_SCORE_SCRATCH_BYTES, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------ core attention
+
+namespace {
+
+// The checks that the cache's calls share (what: the entry point, for the message).
+lsa_status check_cache(const char *what, int64_t N, int B, int max_pages, int Hq, int H, int D, int page,
+                       int64_t n_pages, int dt, int cdt, const void *k_cache, const void *v_cache,
+                       const float *k_scale, const float *v_scale)
+{
+    LSA_REQUIRE(B > 0 && N >= 0 && max_pages > 0 && n_pages > 0 && Hq > 0 && H > 0,
+                "%s: sizes must be positive", what);
+    if (!((dt == DT_F32 && cdt == DT_F32) || (dt == DT_BF16 && (cdt == DT_BF16 || cdt == DT_FP8))))
+        return fail(LSA_ERR_UNSUPPORTED, "%s: dt and cdt must be F32 and F32, or BF16 and BF16 or FP8_E4M3", what);
+    if (D != 32 && D != 64 && D != 128) return fail(LSA_ERR_UNSUPPORTED, "%s: D must be 32, 64 or 128", what);
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return fail(LSA_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64 or 128", what);
+    LSA_REQUIRE(Hq % H == 0, "%s: H_q must be a multiple of H_kv", what);
+    LSA_REQUIRE(N < (int64_t)1 << 24 && B < 1 << 20 && Hq <= 4096, "%s: N, B or H_q too large", what);
+    LSA_REQUIRE((int64_t)max_pages * page < (int64_t)1 << 31, "%s: max_pages * page_size must be below 2^31", what);
+    LSA_REQUIRE(n_pages < (int64_t)1 << 31 && n_pages * H * page < (int64_t)1 << 40, "%s: too many pages", what);
+    LSA_REQUIRE((cdt == DT_FP8) == (k_scale != nullptr) && (cdt == DT_FP8) == (v_scale != nullptr),
+                "%s: k_scale and v_scale are required for an FP8 cache and must be NULL otherwise", what);
+    LSA_REQUIRE(aligned(k_cache, 16) && aligned(v_cache, 16), "%s: the caches must be 16-byte aligned", what);
+    return LSA_OK;
+}
+
+// Rows of [N][heads][D] with a stride from token to token.
+lsa_status check_rows(const char *what, const char *name, const void *p, int64_t stride, int heads, int D, int dt)
+{
+    LSA_REQUIRE(stride >= (int64_t)heads * D && stride < (int64_t)1 << 32,
+                "%s: %s_stride must be at least heads * D", what, name);
+    LSA_REQUIRE(aligned(p, 16) && stride * (int64_t)elem_bytes(dt) % 16 == 0,
+                "%s: rows of %s must be 16-byte aligned", what, name);
+    return LSA_OK;
+}
+
+template <int DT, bool FP8>
+lsa_status launch_append(AppendArgs &A, cudaStream_t st)
+{
+    const int64_t rows = (A.q ? A.Hq : 0) + (FP8 ? 0 : 2 * A.H);
+    const int64_t units = rows * (A.D / 16);
+    // few tokens: a token's rows are spread over CTAs until there are about four for each SM
+    const int64_t want = (4 * (int64_t)num_sms() + A.N - 1) / A.N, most = (units + APPEND_PAGE_THREADS - 1) / APPEND_PAGE_THREADS;
+    A.row_ctas_per_token = (int)(want < most ? want : most);
+    A.row_ctas = A.N * A.row_ctas_per_token;
+    const int64_t jobs = FP8 ? (A.N / A.page + 2 * (int64_t)A.B) * A.H * 2 : 0;
+    const int64_t grid = A.row_ctas + jobs;
+    LSA_REQUIRE(grid < (int64_t)1 << 31, "lsa_kv_append: too many rows for one launch");
+    if (grid == 0) return LSA_OK;
+    k_kv_append<DT, FP8><<<(unsigned)grid, APPEND_PAGE_THREADS, sizeof(float2) * (size_t)(A.rot / 2), st>>>(A);
+    return launched("append to the window cache");
+}
+
+template <int QT, int CT>
+lsa_status launch_attn_rows(const AttnArgs &A, cudaStream_t st)
+{
+    const dim3 grid((unsigned)A.N, (unsigned)((A.Hq + ATTN_ROW_WARPS - 1) / ATTN_ROW_WARPS));
+    k_attn_rows<QT, CT><<<grid, 32 * ATTN_ROW_WARPS, 0, st>>>(A);
+    return launched("attention (rows)");
+}
+
+lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void *workspace, size_t workspace_bytes,
+                     size_t need, cudaStream_t st)
+{
+    LSA_REQUIRE(A.q && A.q_offsets && A.cache_len && A.page_table && A.k_cache && A.v_cache && A.out,
+                "%s: null pointer", what);
+    LSA_TRY(check_cache(what, A.N, A.B, A.max_pages, A.Hq, A.H, A.D, A.page, A.n_pages, dt, cdt, A.k_cache, A.v_cache,
+                        A.k_scale, A.v_scale));
+    LSA_TRY(check_rows(what, "q", A.q, A.q_stride, A.Hq, A.D, dt));
+    LSA_REQUIRE(aligned(A.out, 16), "%s: out must be 16-byte aligned", what);
+    LSA_REQUIRE(A.window >= 0 && A.n_sink >= 0, "%s: window and n_sink must not be negative", what);
+    LSA_REQUIRE(A.scale - A.scale == 0.f, "%s: softmax_scale must be finite", what);
+    if (!workspace || workspace_bytes < need) return fail(LSA_ERR_WORKSPACE, "%s: workspace needs %zu bytes", what, need);
+    LSA_REQUIRE(aligned(workspace, 256), "%s: workspace must be 256-byte aligned", what);
+    if (A.N == 0) return ok();
+    if (dt == DT_F32) LSA_TRY((launch_attn_rows<DT_F32, DT_F32>(A, st)));
+    else if (cdt == DT_BF16) LSA_TRY((launch_attn_rows<DT_BF16, DT_BF16>(A, st)));
+    else LSA_TRY((launch_attn_rows<DT_BF16, DT_FP8>(A, st)));
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N, int B,
+                         const int32_t *cache_len, const int32_t *page_table, int max_pages, const float *inv_freq,
+                         int rot_dim, int interleaved, int H_q, int H_kv, int D, int page_size, int64_t n_pages,
+                         void *k_cache, void *v_cache, lsa_dtype cdt, float *k_scale, float *v_scale, void *q_out,
+                         lsa_stream_t stream)
+{
+    const char *what = "lsa_kv_append";
+    LSA_REQUIRE(k && v && q_offsets && cache_len && page_table && k_cache && v_cache, "%s: null pointer", what);
+    LSA_REQUIRE((q == nullptr) == (q_out == nullptr), "%s: q and q_out are given together", what);
+    LSA_TRY(check_cache(what, N, B, max_pages, H_q, H_kv, D, page_size, n_pages, dt, cdt, k_cache, v_cache, k_scale,
+                        v_scale));
+    LSA_REQUIRE(rot_dim >= 0 && rot_dim <= D, "%s: rot_dim must be in [0, D]", what);
+    if (rot_dim % 16) return fail(LSA_ERR_UNSUPPORTED, "%s: rot_dim must be a multiple of 16", what);
+    LSA_REQUIRE((rot_dim > 0) == (inv_freq != nullptr), "%s: inv_freq is given exactly when rot_dim > 0", what);
+    LSA_TRY(check_rows(what, "k", k, k_stride, H_kv, D, dt));
+    LSA_TRY(check_rows(what, "v", v, v_stride, H_kv, D, dt));
+    if (q) {
+        LSA_TRY(check_rows(what, "q", q, q_stride, H_q, D, dt));
+        LSA_REQUIRE(aligned(q_out, 16), "%s: q_out must be 16-byte aligned", what);
+        const uintptr_t a0 = (uintptr_t)q, a1 = a0 + (uintptr_t)(N > 0 ? ((N - 1) * q_stride + (int64_t)H_q * D) : 0) * elem_bytes(dt);
+        const uintptr_t b0 = (uintptr_t)q_out, b1 = b0 + (uintptr_t)(N * H_q * D) * elem_bytes(dt);
+        LSA_REQUIRE(a1 <= b0 || b1 <= a0 || (q == q_out && q_stride == (int64_t)H_q * D),
+                    "%s: q and q_out overlap", what);
+    }
+    if (N == 0) return ok();
+    AppendArgs A = {};
+    A.q = q; A.k = k; A.v = v;
+    A.q_stride = q_stride; A.k_stride = k_stride; A.v_stride = v_stride;
+    A.q_offsets = q_offsets; A.cache_len = cache_len; A.page_table = page_table; A.inv_freq = inv_freq;
+    A.q_out = q_out; A.k_cache = k_cache; A.v_cache = v_cache; A.k_scale = k_scale; A.v_scale = v_scale;
+    A.N = N; A.n_pages = n_pages; A.B = B; A.max_pages = max_pages; A.Hq = H_q; A.H = H_kv; A.D = D;
+    A.page = page_size; A.rot = rot_dim; A.interleaved = interleaved != 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (dt == LSA_F32) LSA_TRY((launch_append<DT_F32, false>(A, st)));
+    else if (cdt == LSA_BF16) LSA_TRY((launch_append<DT_BF16, false>(A, st)));
+    else LSA_TRY((launch_append<DT_BF16, true>(A, st)));
+    return ok();
+}
+
+size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D)
+{
+    if (N < 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || D <= 0) return 0;
+    return 256;
+}
+
+lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N,
+                                int B, const int32_t *cache_len, const int32_t *page_table, int max_pages, int H_q,
+                                int H_kv, int D, int page_size, int64_t n_pages, const void *k_cache,
+                                const void *v_cache, lsa_dtype cdt, const float *k_scale, const float *v_scale,
+                                int window, int n_sink, float softmax_scale, void *out, float *lse_out,
+                                void *workspace, size_t workspace_bytes, lsa_stream_t stream)
+{
+    AttnArgs A = {};
+    A.q = q; A.q_stride = q_stride; A.q_offsets = q_offsets; A.cache_len = cache_len; A.page_table = page_table;
+    A.k_cache = k_cache; A.v_cache = v_cache; A.k_scale = k_scale; A.v_scale = v_scale; A.out = out; A.lse = lse_out;
+    A.N = N; A.n_pages = n_pages; A.B = B; A.max_pages = max_pages; A.Hq = H_q; A.H = H_kv; A.D = D;
+    A.page = page_size; A.window = window; A.n_sink = n_sink; A.scale = softmax_scale;
+    return attention("lsa_window_attention", A, dt, cdt, workspace, workspace_bytes,
+                     lsa_window_attention_workspace_size(N, B, H_q, H_kv, D), (cudaStream_t)stream);
+}
+
+size_t lsa_core_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D, int k)
+{
+    if (N < 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || D <= 0 || k < 0) return 0;
+    return 256;
+}
+
+lsa_status lsa_core_attention(const void *q, int64_t q_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N,
+                              int B, const int32_t *cache_len, const int32_t *page_table, int max_pages, int H_q,
+                              int H_kv, int D, int page_size, int64_t n_pages, const void *k_cache,
+                              const void *v_cache, int window, int n_sink, float softmax_scale,
+                              const int32_t *topk_idx, int k, const int32_t *idx, const int32_t *count,
+                              const int64_t *seq_offsets, int64_t total_S, const void *hot_kv, size_t row_bytes,
+                              const void *win_kv, int W, void *out, float *lse_out, void *workspace,
+                              size_t workspace_bytes, lsa_stream_t stream)
+{
+    const char *what = "lsa_core_attention";
+    LSA_REQUIRE(topk_idx && idx && count && seq_offsets && hot_kv, "%s: null pointer", what);
+    LSA_REQUIRE(k >= 1 && k <= LSA_MAX_TOPK, "%s: k must be in [1, %d]", what, LSA_MAX_TOPK);
+    LSA_REQUIRE(total_S >= 0 && total_S < (int64_t)1 << 31, "%s: total_S must be in [0, 2^31)", what);
+    LSA_REQUIRE(W >= 0 && (W == 0) == (win_kv == nullptr), "%s: win_kv is given exactly when W > 0", what);
+    LSA_REQUIRE(dt == LSA_F32 || dt == LSA_BF16, "%s: dt must be F32 or BF16", what);
+    LSA_REQUIRE(H_kv > 0 && D > 0 && row_bytes == 2 * (size_t)H_kv * D * elem_bytes(dt),
+                "%s: row_bytes must be 2 * H_kv * D elements", what);
+    LSA_REQUIRE(aligned(hot_kv, 16) && aligned(win_kv, 16), "%s: rows must be 16-byte aligned", what);
+    AttnArgs A = {};
+    A.q = q; A.q_stride = q_stride; A.q_offsets = q_offsets; A.cache_len = cache_len; A.page_table = page_table;
+    A.k_cache = k_cache; A.v_cache = v_cache; A.out = out; A.lse = lse_out;
+    A.N = N; A.n_pages = n_pages; A.B = B; A.max_pages = max_pages; A.Hq = H_q; A.H = H_kv; A.D = D;
+    A.page = page_size; A.window = window; A.n_sink = n_sink; A.scale = softmax_scale;
+    A.topk_idx = topk_idx; A.idx = idx; A.count = count; A.seq_offsets = seq_offsets;
+    A.hot_kv = (const uint8_t *)hot_kv; A.win_kv = (const uint8_t *)win_kv;
+    A.total_S = total_S; A.row_bytes = (int64_t)row_bytes; A.k = k; A.W = W;
+    return attention(what, A, dt, dt, workspace, workspace_bytes,
+                     lsa_core_attention_workspace_size(N, B, H_q, H_kv, D, k), (cudaStream_t)stream);
 }
 
 }  // extern "C"
