@@ -9,8 +9,7 @@
 // An E4M3 page and head carries one scale for its keys and one for its values: the former multiplies
 // the score, the latter the probability.
 //
-// This file: the arguments, and the plain kernel (one warp per query row, fp32 throughout), which takes
-// every type, head size and mask.
+// This file: the arguments, and what the kernels share.
 #pragma once
 #include "kv_append.cuh"
 
@@ -55,12 +54,6 @@ __host__ __device__ __forceinline__ Span visible_span(int64_t p, int window, int
     return s;
 }
 
-// Sequence, position and length of the cache for query token n, checked (false: nothing to do, or bad data).
-struct QueryToken {
-    int b;
-    int64_t pos;
-};
-
 // A page scale must be finite, >= 0; a value scale's reciprocal and its product with a long sum are formed
 // in fp32, so one that is not zero lies in [2^-100, 2^120].
 __device__ __forceinline__ bool good_scale(float s) { return s == 0.f || (s >= 7.8886090522101181e-31f && s <= 1.329227995784916e36f); }
@@ -92,128 +85,6 @@ __device__ __forceinline__ const uint8_t *entry_row(const AttnArgs &A, int b, in
     if (lo < cnt && __ldg(A.idx + off + lo) == e) return A.hot_kv + (off + lo) * A.row_bytes;
     flag(ERRF_INDEX);
     return nullptr;
-}
-
-// Key and value rows of one cached token of head h, with their page's scales (false: the page is bad, flagged).
-template <int CT>
-__device__ __forceinline__ bool cached_rows(const AttnArgs &A, int b, int h, int64_t pos, const uint8_t *&k,
-                                            const uint8_t *&v, float &ks, float &vs)
-{
-    const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, pos / A.page);
-    if (page < 0) return false;
-    const int64_t ph = (int64_t)page * A.H + h;
-    const int64_t e = (ph * A.page + pos % A.page) * A.D;
-    constexpr int bytes = CT == DT_F32 ? 4 : (CT == DT_BF16 ? 2 : 1);
-    k = (const uint8_t *)A.k_cache + e * bytes;
-    v = (const uint8_t *)A.v_cache + e * bytes;
-    ks = vs = 1.f;
-    if constexpr (CT == DT_FP8) {
-        ks = __ldg(A.k_scale + ph);
-        vs = __ldg(A.v_scale + ph);
-        if (!good_scale(ks) || !good_scale(vs)) {
-            flag(ERRF_SCALE);
-            return false;
-        }
-    }
-    return true;
-}
-
-template <int CT>
-__device__ __forceinline__ float cache_elem(const uint8_t *row, int i)
-{
-    return load_elem<CT>(row, i);
-}
-
-constexpr int ATTN_ROW_WARPS = 4;
-constexpr int ATTN_MAX_D = 128;
-
-// One query row (token n, head hq) by one warp: 32 keys at a time, a key per lane for the scores, D / 32
-// dimensions per lane for the values.  qs: the warp's D floats of shared memory.
-template <int QT, int CT>
-__device__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
-{
-    const int lane = threadIdx.x & 31;
-    const int h = hq / (A.Hq / A.H), D = A.D, per = D / 32;
-    for (int i = lane; i < D; i += 32) qs[i] = load_elem<QT>(A.q, n * A.q_stride + (int64_t)hq * D + i);
-    __syncwarp();
-    const Span sp = visible_span(pos, A.window, A.n_sink);
-    const int64_t total = sp.total + A.k;
-    float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
-#pragma unroll
-    for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;
-    for (int64_t t0 = 0; t0 < total; t0 += 32) {
-        const int64_t t = t0 + lane;
-        const uint8_t *kr = nullptr, *vr = nullptr;
-        float ks = 1.f, vs = 1.f;
-        bool there = false, row = false;
-        if (t < sp.total) {
-            there = cached_rows<CT>(A, b, h, t < sp.sinks ? t : sp.lo + (t - sp.sinks), kr, vr, ks, vs);
-        } else if (t < total) {
-            const int32_t e = __ldg(A.topk_idx + n * A.k + (t - sp.total));
-            if (e >= 0) {
-                const uint8_t *r = entry_row(A, b, e);
-                if (r) {
-                    constexpr int bytes = QT == DT_F32 ? 4 : 2;
-                    kr = r + (int64_t)h * D * bytes;
-                    vr = r + (int64_t)(A.H + h) * D * bytes;
-                    there = row = true;
-                }
-            }
-        }
-        float s = -INFINITY;
-        if (there) {
-            float d = 0.f;
-            if (row)
-                for (int i = 0; i < D; i++) d += qs[i] * cache_elem<QT>(kr, i);
-            else
-                for (int i = 0; i < D; i++) d += qs[i] * cache_elem<CT>(kr, i);
-            s = d * (A.scale * ks);
-        }
-        float mx = s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = __expf(m - ref);
-        const float p = there ? __expf(s - ref) : 0.f;
-        l = l * f + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= f;
-        const int many = (int)min((int64_t)32, total - t0);
-        for (int j = 0; j < many; j++) {
-            const float pj = __shfl_sync(0xffffffffu, p * vs, j);
-            const uint8_t *rj = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)vr, j);
-            const bool hot = __shfl_sync(0xffffffffu, (int)row, j) != 0;
-            if (!rj) continue;
-#pragma unroll
-            for (int i = 0; i < ATTN_MAX_D / 32; i++)
-                if (i < per) acc[i] += pj * (hot ? cache_elem<QT>(rj, lane + 32 * i) : cache_elem<CT>(rj, lane + 32 * i));
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < ATTN_MAX_D / 32; i++)
-        if (i < per) store_elem<QT>(A.out, (n * A.Hq + hq) * D + lane + 32 * i, acc[i] * inv);
-    if (A.lse && lane == 0) A.lse[n * A.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
-    __syncwarp();
-}
-
-// Grid: (N, head groups of ATTN_ROW_WARPS).
-template <int QT, int CT>
-__global__ void __launch_bounds__(32 * ATTN_ROW_WARPS) k_attn_rows(const AttnArgs A)
-{
-    __shared__ int slot;
-    __shared__ float qs[ATTN_ROW_WARPS][ATTN_MAX_D];
-    const int64_t n = blockIdx.x;
-    const int b = block_seq_of_token(A.q_offsets, A.B, A.N, n, &slot);
-    if (b >= A.B) return;  // a row behind the last sequence: left as it is
-    const int64_t len = __ldg(A.cache_len + b);
-    const int hq = blockIdx.y * ATTN_ROW_WARPS + (threadIdx.x >> 5);
-    if (len < 0 && threadIdx.x == 0) flag(ERRF_COUNT);
-    if (hq < A.Hq)
-        attend_row<QT, CT>(A, b, len < 0 ? -1 : len + (n - __ldg(A.q_offsets + b)), n, hq, qs[threadIdx.x >> 5]);
 }
 
 }  // namespace lsa

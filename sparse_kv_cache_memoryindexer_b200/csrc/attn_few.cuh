@@ -1,0 +1,1037 @@
+// Core attention for few query rows: decode steps, small groups of tokens, every type and head size.
+//
+// A tile is 16 query rows of one sequence and key/value head (rows are token-major, the G = Hq / H heads
+// of a group inside a token); its keys come in chunks of 16 positions, aligned, so a chunk lies in one
+// page and its 16 rows are contiguous.  With so few rows the time goes into reading keys and values once
+// (HBM), so the kernel is built around loads in flight: every warp walks chunks of its own with its own
+// ring of stages (cp.async, 16 bytes a lane), the 16 rows of the tile in its registers, and never waits
+// for another warp until the tile's end, where the warps' running maxima, sums and outputs are joined.
+// The products are warp MMAs: 16 rows are one m16 tile, and the tensor pipe is far from its limit here
+// (32 MMAs for the 8 KB of a bf16 chunk), so nothing is gained by staging them through TMEM.
+//   bf16 cache:  m16n8k16 bf16, probabilities rounded to bf16 (their sum is taken before that).
+//   E4M3 cache:  codes decoded exactly to f16; the query row is brought to f16 by a power of two of its
+//                own (elements 2^33 times smaller than the row's largest lose bits, no others).  A page's
+//                value scale vs enters the exponent: p' = 2^(s + log2 vs - m'), with m' the running maximum
+//                of s + log2 vs, so p' is rounded to f16 relative to what it adds to the output whatever the
+//                scales; the softmax sum takes p' / vs in fp32.  p' is kept 2^15 times larger (below f16's
+//                largest), so that only weights under 2^-29 of the largest are subnormal and lose bits.
+//   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
+//                (the fourth, lo lo, is below 2^-22 of the product).
+//
+// Work is either one CTA per tile, or split over keys: the chunks of all tiles of all sequences form one
+// range that the CTAs share evenly (whatever the lengths), a CTA's part of a tile that it does not hold
+// whole goes to the workspace and k_attn_join adds the parts in order.  A CTA leaves at most two parts.
+#pragma once
+#include "attn.cuh"
+#include "pdl.cuh"
+
+namespace lsa {
+
+namespace few {
+
+constexpr int WARPS = 4;
+constexpr int ROWS = 16;
+constexpr int KEYS = 16;
+constexpr int JOIN_ROWS = 4;       // rows of a tile per CTA of k_attn_join
+
+template <int CT, int D>
+struct Cfg {
+    static constexpr int EB = CT == DT_F32 ? 4 : (CT == DT_BF16 ? 2 : 1);
+    static constexpr int RB = D * EB;               // bytes of a key or value row
+    static constexpr int CHUNK = 2 * KEYS * RB;     // keys, then values
+    static constexpr int STAGES = CT == DT_FP8 ? 4 : 3;
+    static constexpr int RING = WARPS * STAGES * CHUNK;
+    static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
+    static constexpr int NT = D / 8;                // n-tiles of the value product
+    static constexpr int QREGS = CT == DT_F32 ? D / 2 : D / 4;  // query fragment registers
+    static constexpr int SMEM = RING + WARPS * (ROWS * KEYS * 4) + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 16;
+};
+
+// 16-byte piece of a row that holds piece c of row `row`: chosen for each access pattern below so that the
+// eight lanes of a phase fall on different banks.
+template <int CT, int D>
+__device__ __forceinline__ int swz(int row, int c)
+{
+    if constexpr (CT == DT_BF16) return D >= 64 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+    else if constexpr (CT == DT_F32 || D == 128) return c ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2));
+    else if constexpr (D == 64) return c ^ (((row >> 1) & 1) << 1);
+    else return c;
+}
+
+// Byte offset of element i of row `row` in a swizzled chunk.
+template <int CT, int D>
+__device__ __forceinline__ uint32_t elem_off(int row, int i)
+{
+    using C = Cfg<CT, D>;
+    const int byte = i * C::EB;
+    return (uint32_t)(row * C::RB + swz<CT, D>(row, byte >> 4) * 16 + (byte & 15));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, both tf32 (hi is x without its low bits' rounding; lo the rest, rounded).
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo)
+{
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma_3xtf32(float (&d)[4], const float (&a)[4], float b0, float b1)
+{
+    uint32_t ah[4], al[4], bh0, bl0, bh1, bl1;
+#pragma unroll
+    for (int i = 0; i < 4; i++) split_tf32(a[i], ah[i], al[i]);
+    split_tf32(b0, bh0, bl0);
+    split_tf32(b1, bh1, bl1);
+    mma_tf32(d, al, bh0, bh1);
+    mma_tf32(d, ah, bl0, bl1);
+    mma_tf32(d, ah, bh0, bh1);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Two E4M3 codes to two f16 (exact; a NaN code stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack_b16x2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Dimension that k-step ks of the score product puts in slot e of the lanes of column c (E4M3: the order of
+// the dimensions in the contraction is free, this one lets a lane read its codes 16 bytes at a time).
+template <int D>
+__device__ __forceinline__ int e4m3_dim(int ks, int c, int e)
+{
+    return D >= 64 ? 16 * (c + 4 * (ks / 4)) + 4 * (ks % 4) + e : 8 * c + 4 * ks + e;
+}
+
+// Dimension of accumulator element e (0: first column, 1: second) of n-tile t of the value product.
+template <int CT>
+__device__ __forceinline__ int out_dim(int t, int c, int e)
+{
+    if constexpr (CT == DT_BF16) return 8 * t + 2 * c + e;
+    else return 32 * (t / 4) + 4 * (2 * c + e) + t % 4;
+}
+
+// Query fragments of rows r and r + 8 (null: a row that is not there), and the factor of each row's scores.
+template <int CT, int D>
+__device__ __forceinline__ void load_q(const void *const (&row)[2], int c, uint32_t (&q)[Cfg<CT, D>::QREGS], float (&f)[2])
+{
+    f[0] = f[1] = 1.f;
+    if constexpr (CT == DT_BF16) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {  // a0: row r, k 2c; a1: row r + 8; a2, a3: k 2c + 8
+                const uint32_t *p = (const uint32_t *)row[i & 1];
+                q[4 * ks + i] = p ? __ldg(p + (16 * ks + 8 * (i >> 1) + 2 * c) / 2) : 0u;
+            }
+    } else if constexpr (CT == DT_FP8) {
+        float mx[2] = {0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t *p = (const uint32_t *)row[i & 1];
+                const uint32_t w = p ? __ldg(p + e4m3_dim<D>(ks, c, 2 * (i >> 1)) / 2) : 0u;
+                q[4 * ks + i] = w;
+                mx[i & 1] = fmaxf(mx[i & 1], fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xFFFF0000u))));
+            }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            // 2^(8 - exponent of the row's largest): its element comes to [2^8, 2^9)
+            int e = 8 - ((int)(__float_as_uint(mx[i]) >> 23) - 127);
+            e = e > 120 ? 120 : (e < -120 ? -120 : e);
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            f[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    uint32_t &w = q[4 * ks + 2 * k + i];
+                    w = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+                }
+        }
+    } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 8; ks++)  // k-steps of 8: slots c and c + 4 are dimensions 2 (ks % 2) + {0, 1} of the lane's four
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float *p = (const float *)row[i & 1];
+                q[4 * ks + i] = p ? __float_as_uint(__ldg(p + 16 * (ks / 2) + 4 * c + 2 * (ks % 2) + (i >> 1))) : 0u;
+            }
+    }
+}
+
+// s[j] += query rows . keys 8j .. 8j + 7 of the chunk at shared address kb.
+template <int CT, int D>
+__device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, D>::QREGS], float (&s)[2][4])
+{
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    if constexpr (CT == DT_BF16) {
+        // matrices of ldmatrix: keys 0-7 and dims 0-7, keys 0-7 and dims 8-15, then keys 8-15
+        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++) {
+            uint32_t b[4];
+            ldsm4(b, kb + (uint32_t)(row * Cfg<CT, D>::RB + swz<CT, D>(row, 2 * ks + half) * 16));
+            const uint32_t a[4] = {q[4 * ks], q[4 * ks + 1], q[4 * ks + 2], q[4 * ks + 3]};
+            mma_bf16(s[0], a, b[0], b[1]);
+            mma_bf16(s[1], a, b[2], b[3]);
+        }
+    } else if constexpr (CT == DT_FP8) {
+#pragma unroll
+        for (int hh = 0; hh < (D >= 64 ? D / 64 : 1); hh++) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int row = r + 8 * j;
+                if constexpr (D >= 64) {
+                    const uint4 v = lds128(kb + (uint32_t)(row * D + swz<CT, D>(row, c + 4 * hh) * 16));
+                    w[j][0] = v.x; w[j][1] = v.y; w[j][2] = v.z; w[j][3] = v.w;
+                } else {
+                    const uint2 v = lds64(kb + (uint32_t)(row * D + c * 8));
+                    w[j][0] = v.x; w[j][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < (D >= 64 ? 4 : 2); t++) {
+                const int ks = 4 * hh + t;
+                const uint32_t a[4] = {q[4 * ks], q[4 * ks + 1], q[4 * ks + 2], q[4 * ks + 3]};
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    mma_f16(s[j], a, e4m3x2_to_f16x2(w[j][t]), e4m3x2_to_f16x2(w[j][t] >> 16));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < D / 16; g++) {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int row = r + 8 * j;
+                const uint4 v = lds128(kb + (uint32_t)(row * Cfg<CT, D>::RB + swz<CT, D>(row, 4 * g + c) * 16));
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const int ks = 2 * g + t;
+                    const float a[4] = {__uint_as_float(q[4 * ks]), __uint_as_float(q[4 * ks + 1]),
+                                        __uint_as_float(q[4 * ks + 2]), __uint_as_float(q[4 * ks + 3])};
+                    mma_3xtf32(s[j], a, __uint_as_float(t ? v.z : v.x), __uint_as_float(t ? v.w : v.y));
+                }
+            }
+        }
+    }
+}
+
+// acc += p (16 rows x 16 keys, as the score product leaves them) . values at shared address vb.
+template <int CT, int D>
+__device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], float (&acc)[Cfg<CT, D>::NT][4])
+{
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    if constexpr (CT == DT_BF16) {
+        const uint32_t a[4] = {pack_b16x2(p[0][0], p[0][1]), pack_b16x2(p[0][2], p[0][3]), pack_b16x2(p[1][0], p[1][1]),
+                               pack_b16x2(p[1][2], p[1][3])};
+        const int row = lane & 15;
+#pragma unroll
+        for (int t = 0; t < D / 16; t++) {  // keys 0-7, 8-15 of dims 16t .. + 7, then of dims 16t + 8 .. + 15
+            uint32_t b[4];
+            ldsm4t(b, vb + (uint32_t)(row * Cfg<CT, D>::RB + swz<CT, D>(row, 2 * t + (lane >> 4)) * 16));
+            mma_bf16(acc[2 * t], a, b[0], b[1]);
+            mma_bf16(acc[2 * t + 1], a, b[2], b[3]);
+        }
+    } else if constexpr (CT == DT_FP8) {
+        const uint32_t a[4] = {pack_f16x2(p[0][0], p[0][1]), pack_f16x2(p[0][2], p[0][3]), pack_f16x2(p[1][0], p[1][1]),
+                               pack_f16x2(p[1][2], p[1][3])};
+#pragma unroll
+        for (int blk = 0; blk < D / 32; blk++) {
+            uint32_t w[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of dims 32 blk + 4r .. + 3
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int row = 2 * c + (j & 1) + 8 * (j >> 1);
+                w[j] = lds32(vb + (uint32_t)(row * D + swz<CT, D>(row, 2 * blk + (r >> 2)) * 16 + (r & 3) * 4));
+            }
+            // pairs of codes (key, key + 1) for dims 0, 1 and 2, 3 of the four
+            const uint32_t x0 = __byte_perm(w[0], w[1], 0x5140), x1 = __byte_perm(w[0], w[1], 0x7362);
+            const uint32_t y0 = __byte_perm(w[2], w[3], 0x5140), y1 = __byte_perm(w[2], w[3], 0x7362);
+            mma_f16(acc[4 * blk], a, e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
+            mma_f16(acc[4 * blk + 1], a, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
+            mma_f16(acc[4 * blk + 2], a, e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
+            mma_f16(acc[4 * blk + 3], a, e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; j++) {  // k-step j: slots c, c + 4 are keys 8j + 2c, + 1
+            const float a[4] = {p[j][0], p[j][2], p[j][1], p[j][3]};
+#pragma unroll
+            for (int blk = 0; blk < D / 32; blk++) {
+                const int row = 8 * j + 2 * c;
+                const uint4 x = lds128(vb + (uint32_t)(row * Cfg<CT, D>::RB + swz<CT, D>(row, 8 * blk + r) * 16));
+                const uint4 y = lds128(vb + (uint32_t)((row + 1) * Cfg<CT, D>::RB + swz<CT, D>(row + 1, 8 * blk + r) * 16));
+                mma_3xtf32(acc[4 * blk], a, __uint_as_float(x.x), __uint_as_float(y.x));
+                mma_3xtf32(acc[4 * blk + 1], a, __uint_as_float(x.y), __uint_as_float(y.y));
+                mma_3xtf32(acc[4 * blk + 2], a, __uint_as_float(x.z), __uint_as_float(y.z));
+                mma_3xtf32(acc[4 * blk + 3], a, __uint_as_float(x.w), __uint_as_float(y.w));
+            }
+        }
+    }
+}
+
+template <int CT, int D>
+__device__ __forceinline__ float smem_elem(const uint8_t *chunk, int row, int i)
+{
+    const uint8_t *p = chunk + elem_off<CT, D>(row, i);
+    if constexpr (CT == DT_F32) return *(const float *)p;
+    else if constexpr (CT == DT_BF16) return bf16_bits_to_float(*(const uint16_t *)p);
+    else return e4m3_to_float(*p);
+}
+
+// Whether a chunk of values holds an infinity or NaN (the whole warp asks).
+template <int CT, int D>
+__device__ __forceinline__ bool any_nonfinite(uint32_t vb)
+{
+    bool bad = false;
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < Cfg<CT, D>::RB; i += 32) {
+        const uint4 v = lds128(vb + (uint32_t)i * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+            if constexpr (CT == DT_F32) bad |= (w[t] & 0x7F800000u) == 0x7F800000u;
+            else if constexpr (CT == DT_BF16)
+                bad |= (w[t] & 0x7F80u) == 0x7F80u || (w[t] & 0x7F800000u) == 0x7F800000u;
+            else
+                bad |= __vcmpeq4(w[t] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+        }
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+// acc += p . values key by key, skipping a row's masked keys (p = 0): for a chunk in which a key that some rows
+// must not see holds an infinity or NaN, which a matrix product would carry into them as 0 x inf.
+template <int CT, int D>
+__device__ __noinline__ void values_by_key(const uint8_t *chunk, float *ps, const float (&p)[2][4], float (&acc)[Cfg<CT, D>::NT][4])
+{
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) ps[(r + 8 * (e >> 1)) * KEYS + 8 * j + 2 * c + (e & 1)] = p[j][e];
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 0; k < KEYS; k++) {
+        const float p0 = ps[r * KEYS + k], p1 = ps[(r + 8) * KEYS + k];
+#pragma unroll
+        for (int t = 0; t < Cfg<CT, D>::NT; t++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float v = smem_elem<CT, D>(chunk, k, out_dim<CT>(t, c, e));
+                if (p0 != 0.f) acc[t][e] += p0 * v;
+                if (p1 != 0.f) acc[t][2 + e] += p1 * v;
+            }
+    }
+    __syncwarp();
+}
+
+// --------------------------------------------------------------------------------------- the work
+
+// What the tiles of one sequence share.  Chunks are numbered [first tokens][window]: chunk u < sc is positions
+// 16 u .., the others 16 (wc0 + u - sc) .., up to `chunks`; then the chunks of the Top-k list.
+struct Seq {
+    int64_t off;    // first query token
+    int64_t n;      // query tokens
+    int64_t len;    // tokens before this call's
+    int tiles;      // tiles of 16 rows
+    int sc, wc0;
+    int chunks;     // of the cache
+    int total;      // with the Top-k list's
+};
+
+__device__ __forceinline__ int tiles_per_token(const AttnArgs &A) { return (A.Hq / A.H + ROWS - 1) / ROWS; }
+
+template <bool CORE>
+__device__ __forceinline__ Seq load_seq(const AttnArgs &A, int b)
+{
+    Seq s = {};
+    const int64_t lo = __ldg(A.q_offsets + b), hi = __ldg(A.q_offsets + b + 1);
+    if (lo < 0 || hi < lo || hi > A.N) {
+        flag(ERRF_OFFSETS);
+        return s;
+    }
+    s.off = lo;
+    s.n = hi - lo;
+    s.len = __ldg(A.cache_len + b);
+    if (s.n == 0) return s;
+    const int G = A.Hq / A.H;
+    s.tiles = CORE ? (int)s.n * tiles_per_token(A) : (int)((s.n * G + ROWS - 1) / ROWS);
+    if (s.len < 0) {
+        flag(ERRF_COUNT);
+        s.len = -s.n;  // every query stands before position 0: nothing to see
+    }
+    const int64_t limit = (int64_t)A.max_pages * A.page;
+    int64_t last = s.len + s.n - 1;
+    if (last >= limit) {
+        flag(ERRF_COUNT);
+        last = limit - 1;
+    }
+    const Span first = visible_span(s.len < 0 ? 0 : s.len, A.window, A.n_sink);
+    s.wc0 = (int)(first.lo / KEYS);
+    const int sink_chunks = (int)((first.sinks + KEYS - 1) / KEYS);
+    s.sc = sink_chunks < s.wc0 ? sink_chunks : s.wc0;
+    const int64_t wend = last < 0 ? 0 : last / KEYS + 1;
+    s.chunks = s.sc + (wend > s.wc0 ? (int)(wend - s.wc0) : 0);
+    if (s.sc > limit / KEYS) s.sc = s.chunks = (int)(limit / KEYS);
+    s.total = s.chunks + (CORE ? (A.k + KEYS - 1) / KEYS : 0);
+    if (s.total < 1) s.total = 1;  // a tile without keys still writes its rows
+    return s;
+}
+
+// One tile: 16 rows of a sequence and head.
+struct Tile {
+    int64_t n0;      // CORE: its token; else the sequence's first token
+    int64_t p_lo, p_hi;  // positions of its first and last row's tokens
+    int row0;        // first row (token-major within the sequence; CORE: first head of the group)
+    int rows;
+};
+
+template <bool CORE>
+__device__ __forceinline__ Tile make_tile(const AttnArgs &A, const Seq &s, int tile)
+{
+    Tile t;
+    const int G = A.Hq / A.H;
+    if constexpr (CORE) {
+        const int tpt = tiles_per_token(A);
+        t.n0 = s.off + tile / tpt;
+        t.row0 = (tile % tpt) * ROWS;
+        t.rows = min(ROWS, G - t.row0);
+        t.p_lo = t.p_hi = s.len + tile / tpt;
+    } else {
+        t.n0 = s.off;
+        t.row0 = tile * ROWS;
+        t.rows = (int)min((int64_t)ROWS, s.n * G - t.row0);
+        t.p_lo = s.len + t.row0 / G;
+        t.p_hi = s.len + (t.row0 + t.rows - 1) / G;
+    }
+    return t;
+}
+
+// Token of row i of the tile, its position, and its head in the group.
+template <bool CORE>
+__device__ __forceinline__ void tile_row(const AttnArgs &A, const Seq &s, const Tile &t, int i, int64_t &n, int64_t &pos, int &g)
+{
+    if constexpr (CORE) {
+        n = t.n0;
+        pos = t.p_lo;
+        g = t.row0 + i;
+    } else {
+        const int G = A.Hq / A.H, R = t.row0 + i;
+        n = t.n0 + R / G;
+        pos = s.len + R / G;
+        g = R % G;
+    }
+}
+
+// A part in the workspace: maxima and sums of 16 rows (of 2^(x - max)), then the sums of values.
+template <int D>
+constexpr size_t part_floats() { return 2 * ROWS + (size_t)ROWS * D; }
+
+// Chunks [u0, u1) of tile `tile` and head h of sequence b, by the whole CTA.  part: where to leave the sums (null:
+// the tile is whole, the outputs are written).
+template <int QT, int CT, int D, bool CORE>
+__device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, int tile, int h, int u0, int u1, float *part,
+                                        const uint8_t *const *sel, uint8_t *smem)
+{
+    using C = Cfg<CT, D>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + warp * C::STAGES * C::CHUNK;
+    const uint32_t ring_a = (uint32_t)__cvta_generic_to_shared(ring);
+    float *ps = (float *)(smem + C::RING) + warp * ROWS * KEYS;
+    float *ml = (float *)(smem + C::RING + WARPS * ROWS * KEYS * 4);
+    struct Meta { float ks, vs; uint32_t live, pad; };
+    Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
+    const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
+
+    const Tile t = make_tile<CORE>(A, s, tile);
+    const int G = A.Hq / A.H;
+    const int64_t low = (A.window > 0 && t.p_lo + 1 > A.window) ? t.p_lo + 1 - A.window : 0;  // first window key of the first row
+
+    // the chunks of this tile among [u0, u1): [u0, min(u1, sc)) and [max(u0, a), min(u1, z)), then the Top-k list's
+    // (first tokens that reach into the window's chunks: none of those is skipped)
+    const int a = A.n_sink > s.wc0 * KEYS ? s.sc : max(s.sc, s.sc + (int)(low / KEYS) - s.wc0);
+    const int z = t.p_hi < 0 ? 0 : (int)min((int64_t)s.chunks, s.sc + t.p_hi / KEYS - s.wc0 + 1);
+    const int e0 = max(0, min(u1, s.sc) - u0);
+    const int b0 = max(u0, a), e1 = max(0, min(u1, z) - b0);
+    const int c0 = max(u0, s.chunks), e2 = CORE ? max(0, u1 - c0) : 0;
+    const int count = t.p_hi < 0 ? (CORE ? e2 : 0) : e0 + e1 + e2;
+    auto chunk_of = [&](int i) -> int {
+        if (t.p_hi < 0) return c0 + i;
+        return i < e0 ? u0 + i : (i < e0 + e1 ? b0 + (i - e0) : c0 + (i - e0 - e1));
+    };
+
+    uint32_t q[C::QREGS];
+    float qf[2];
+    int64_t rpos[2];
+    {
+        const void *rows[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            rows[i] = nullptr;
+            rpos[i] = -1;
+            if (r + 8 * i < t.rows) {
+                int64_t n;
+                int g;
+                tile_row<CORE>(A, s, t, r + 8 * i, n, rpos[i], g);
+                constexpr int qb = QT == DT_F32 ? 4 : 2;
+                rows[i] = (const uint8_t *)A.q + (n * A.q_stride + (int64_t)(h * G + g) * D) * qb;
+            }
+        }
+        load_q<CT, D>(rows, c, q, qf);
+    }
+    const float sl2 = A.scale * 1.4426950408889634f;
+    const float sf[2] = {sl2 * qf[0], sl2 * qf[1]};
+
+    float acc[C::NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < C::NT; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
+
+    // start the loads of the warp's i-th chunk (i counts the CTA's chunks: warp w takes w, w + WARPS, ..)
+    auto issue = [&](int i, int stage) {
+        const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
+        const int u = chunk_of(i);
+        if (!CORE || u < s.chunks) {
+            const int64_t p0 = (int64_t)(u < s.sc ? u : s.wc0 + (u - s.sc)) * KEYS;
+            const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, p0 / A.page);
+            const int64_t ph = (int64_t)max(page, 0) * A.H + h;
+            const int64_t byte = (ph * A.page + p0 % A.page) * C::RB;
+            const uint8_t *kp = (const uint8_t *)A.k_cache + byte, *vp = (const uint8_t *)A.v_cache + byte;
+#pragma unroll
+            for (int x = 0; x < C::RB / 32; x++) {
+                const int piece = lane + 32 * x, row = piece / (C::RB / 16), pc = piece % (C::RB / 16);
+                const int64_t pos = p0 + row;
+                // keys that no row of the tile sees come in as zeros
+                const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
+                const uint32_t o = (uint32_t)(row * C::RB + swz<CT, D>(row, pc) * 16);
+                cp_async16(kb + o, see ? kp + piece * 16 : (const uint8_t *)A.k_cache, see ? 16 : 0);
+                cp_async16(vb + o, see ? vp + piece * 16 : (const uint8_t *)A.v_cache, see ? 16 : 0);
+            }
+            if constexpr (CT == DT_FP8) {
+                if (lane < 2) cp_async4(meta_a + (uint32_t)stage * 16 + lane * 4, (lane ? A.v_scale : A.k_scale) + ph, page >= 0 ? 4 : 0);
+            }
+            if (lane == 0) meta[stage].live = page >= 0 ? 0xFFFFu : 0u;
+        } else {
+            const int j = (u - s.chunks) * KEYS + (lane & 15);
+            const uint8_t *row_p = j < A.k ? (const uint8_t *)__ldg((const unsigned long long *)sel + t.n0 * A.k + j) : nullptr;
+            const uint32_t live = __ballot_sync(0xffffffffu, row_p != nullptr) & 0xFFFFu;
+#pragma unroll
+            for (int x = 0; x < C::RB / 32; x++) {
+                const int piece = lane + 32 * x, row = piece / (C::RB / 16), pc = piece % (C::RB / 16);
+                const uint8_t *p = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)row_p, row);
+                const uint32_t o = (uint32_t)(row * C::RB + swz<CT, D>(row, pc) * 16);
+                cp_async16(kb + o, p ? p + (int64_t)h * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
+                cp_async16(vb + o, p ? p + (int64_t)(A.H + h) * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
+            }
+            if (lane == 0) meta[stage].live = live;
+        }
+    };
+
+#pragma unroll
+    for (int st = 0; st < C::STAGES - 1; st++) {
+        if (warp + st * WARPS < count) issue(warp + st * WARPS, st);
+        cp_commit();
+    }
+    int stage = 0, fill = C::STAGES - 1;
+    for (int i = warp; i < count; i += WARPS) {
+        if (i + (C::STAGES - 1) * WARPS < count) issue(i + (C::STAGES - 1) * WARPS, fill);
+        cp_commit();
+        cp_wait<C::STAGES - 1>();
+        __syncwarp();
+        const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
+        const int u = chunk_of(i);
+        const bool listed = CORE && u >= s.chunks;
+        uint32_t live = meta[stage].live;
+        float ks = 1.f, vs = 1.f, lv = 0.f, inv_vs = 1.f;
+        if constexpr (CT == DT_FP8) {
+            ks = meta[stage].ks;
+            vs = meta[stage].vs;
+            if (live && (!good_scale(ks) || !good_scale(vs))) {
+                if (lane == 0) flag(ERRF_SCALE);
+                live = 0;
+            }
+            if (vs > 0.f) {
+                lv = log2f(vs);
+                inv_vs = 1.f / vs;
+            }
+        }
+        float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        scores<CT, D>(kb, q, x);
+        const int64_t p0 = (int64_t)(u < s.sc ? u : s.wc0 + (u - s.sc)) * KEYS;
+        const bool whole = live == 0xFFFFu &&
+                           (listed || (p0 + KEYS - 1 <= t.p_lo && (A.window == 0 || p0 > t.p_hi - A.window || p0 + KEYS <= A.n_sink)));
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[j][e] = CT == DT_FP8 ? fmaf(x[j][e], sf[e >> 1] * ks, lv) : x[j][e] * sf[e >> 1];
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int key = 8 * j + 2 * c + (e & 1);
+                    const int64_t pos = p0 + key, me = rpos[e >> 1];
+                    const bool see = (live >> key & 1) &&
+                                     (listed || (pos <= me && (A.window == 0 || pos > me - A.window || pos < A.n_sink)));
+                    if (!see) x[j][e] = -INFINITY;
+                }
+        }
+        bool moved = false;
+        float f[2];
+#pragma unroll
+        for (int i2 = 0; i2 < 2; i2++) {
+            float mx = fmaxf(fmaxf(x[0][2 * i2], x[0][2 * i2 + 1]), fmaxf(x[1][2 * i2], x[1][2 * i2 + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[i2], mx);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            f[i2] = exp2_fast(m[i2] - ref);
+            moved |= mn != m[i2];
+            m[i2] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float &v = x[j][2 * i2 + e];
+                    v = exp2_fast(v - (ref - C::SHIFT));
+                    sum += v;
+                }
+            l[i2] = fmaf(l[i2], f[i2], sum * inv_vs);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int i2 = 0; i2 < C::NT; i2++) {
+                acc[i2][0] *= f[0];
+                acc[i2][1] *= f[0];
+                acc[i2][2] *= f[1];
+                acc[i2][3] *= f[1];
+            }
+        }
+        if (live == 0 || (CT == DT_FP8 && vs == 0.f)) {
+            // nothing to add (a value scale of zero: the keys have had their share of the softmax sum)
+        } else if (!CORE && !whole && t.p_lo != t.p_hi && any_nonfinite<CT, D>(vb)) {
+            float px[2][4], o[C::NT][4];  // (copies: the call takes addresses, acc and x stay in registers)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                px[0][e] = x[0][e];
+                px[1][e] = x[1][e];
+#pragma unroll
+                for (int nt = 0; nt < C::NT; nt++) o[nt][e] = acc[nt][e];
+            }
+            values_by_key<CT, D>(ring + stage * C::CHUNK + KEYS * C::RB, ps, px, o);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+#pragma unroll
+                for (int nt = 0; nt < C::NT; nt++) acc[nt][e] = o[nt][e];
+        } else {
+            values<CT, D>(vb, x, acc);
+        }
+        __syncwarp();
+        stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+        fill = fill + 1 == C::STAGES ? 0 : fill + 1;
+    }
+    cp_wait<0>();
+
+    // join the warps: maxima, then every warp's sums brought to the common maximum
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (c == 0) {
+            ml[warp * ROWS + r + 8 * i] = m[i];
+            ml[(WARPS + warp) * ROWS + r + 8 * i] = l[i];
+        }
+    }
+    __syncthreads();
+    float *os = (float *)smem + warp * ROWS * D;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        float M = ml[r + 8 * i];
+#pragma unroll
+        for (int w = 1; w < WARPS; w++) M = fmaxf(M, ml[w * ROWS + r + 8 * i]);
+        const float f = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - M);
+#pragma unroll
+        for (int nt = 0; nt < C::NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) os[(r + 8 * i) * D + out_dim<CT>(nt, c, e)] = acc[nt][2 * i + e] * f;
+    }
+    __syncthreads();
+    constexpr int GROUPS = D / 4;  // four dimensions of a row each
+    for (int i = tid; i < ROWS * GROUPS; i += 32 * WARPS) {
+        const int row = i / GROUPS, d = (i % GROUPS) * 4;
+        if (row >= t.rows) continue;
+        float M = ml[row], L = 0.f;
+#pragma unroll
+        for (int w = 1; w < WARPS; w++) M = fmaxf(M, ml[w * ROWS + row]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) {
+            const float mw = ml[w * ROWS + row];
+            L += ml[(WARPS + w) * ROWS + row] * (mw == -INFINITY ? 0.f : exp2_fast(mw - M));
+            const float4 v = *(const float4 *)((const float *)smem + (w * ROWS + row) * D + d);
+            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+        }
+        if (part) {
+            if (d == 0) {
+                part[row] = M;
+                part[ROWS + row] = L;
+            }
+            *(float4 *)(part + 2 * ROWS + row * D + d) = o;
+        } else {
+            int64_t n, pos;
+            int g;
+            tile_row<CORE>(A, s, t, row, n, pos, g);
+            const int64_t at = n * A.Hq + h * G + g;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            if constexpr (QT == DT_F32)
+                *(float4 *)((float *)A.out + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            else
+                *(uint2 *)((__nv_bfloat16 *)A.out + at * D + d) =
+                    make_uint2(pack_b16x2(o.x * inv, o.y * inv), pack_b16x2(o.z * inv, o.w * inv));
+            if (A.lse && d == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - C::SHIFT + log2f(L)) * 0.6931471805599453f;
+        }
+    }
+    __syncthreads();  // the ring is free again
+}
+
+// Sum over the block of v, and the sum over the threads before this one.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t &before)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int64_t total = 0, base = 0;
+    for (int w = 0; w < warps; w++) {
+        if (w == warp) base = total;
+        total += warp_sums[w];
+    }
+    before = base + x - v;
+    return total;
+}
+
+// Chunks of sequence b's tiles, of all heads.
+__device__ __forceinline__ int64_t seq_cost(const AttnArgs &A, const Seq &s) { return (int64_t)s.tiles * A.H * s.total; }
+
+// Range of CTA c of `ctas` among `total` chunks.
+__device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
+// CTA whose range holds chunk x.
+__device__ __forceinline__ int cta_of(int64_t total, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
+
+// CTAs that share the work: no more than leave MIN_CHUNKS to each.
+constexpr int MIN_CHUNKS = 4 * WARPS;
+__device__ __forceinline__ int sharing_ctas(int64_t total, int grid)
+{
+    const int64_t c = total / MIN_CHUNKS;
+    return c < 1 ? 1 : (c < grid ? (int)c : grid);
+}
+
+template <int QT, int CT, int D, bool CORE, bool SPLIT>
+__global__ void __launch_bounds__(32 * WARPS) k_attn_few(const AttnArgs A, float *parts, const uint8_t *const *sel)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sums[WARPS];
+    __shared__ int found;
+    __shared__ int64_t found_before;
+    if constexpr (!SPLIT) {
+        // one CTA per tile and head; tiles of sequence b are numbered from off_b G / 16 + b (CORE: off_b tiles a token),
+        // so that ranges of ragged sequences do not meet
+        if constexpr (CORE) pdl_wait();
+        const int G = A.Hq / A.H;
+        const int64_t x = blockIdx.x;
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        for (int b = threadIdx.x; b < A.B; b += blockDim.x) {
+            const int64_t lo = __ldg(A.q_offsets + b), hi = __ldg(A.q_offsets + b + 1);
+            if (lo < 0 || hi < lo || hi > A.N) flag(ERRF_OFFSETS);
+            else if (hi > lo && (CORE ? lo * tiles_per_token(A) : lo * G / ROWS + b) <= x) atomicMax(&found, b);
+        }
+        __syncthreads();
+        const int b = found;
+        if (b < 0) return;
+        const Seq s = load_seq<CORE>(A, b);
+        const int64_t tile = x - (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b);
+        if (tile < s.tiles) do_tile<QT, CT, D, CORE>(A, s, b, (int)tile, blockIdx.y, 0, s.total, nullptr, sel, smem);
+    } else {
+        pdl_trigger();
+        int64_t total = 0;
+        for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
+            const int b = b0 + threadIdx.x;
+            int64_t before;
+            total += block_scan(b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0, sums, before);
+        }
+        if constexpr (CORE) pdl_wait();
+        const int ctas = sharing_ctas(total, gridDim.x);
+        if (total == 0 || (int)blockIdx.x >= ctas) return;
+        int64_t x = range_start(total, blockIdx.x, ctas);
+        const int64_t end = range_start(total, blockIdx.x + 1, ctas);
+        // the sequence that holds x
+        int64_t base = 0;
+        if (threadIdx.x == 0) found = -1;
+        for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
+            const int b = b0 + threadIdx.x;
+            const int64_t mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
+            int64_t before;
+            const int64_t sum = block_scan(mine, sums, before);
+            if (mine > 0 && base + before <= x && x < base + before + mine) {
+                found = b;
+                found_before = base + before;
+            }
+            base += sum;
+            __syncthreads();
+            if (found >= 0) break;
+        }
+        int b = found;
+        if (b < 0) return;
+        int64_t seq_start = found_before;
+        Seq s = load_seq<CORE>(A, b);
+        while (x < end) {
+            while (x >= seq_start + seq_cost(A, s)) {
+                seq_start += seq_cost(A, s);
+                if (++b >= A.B) return;
+                s = load_seq<CORE>(A, b);
+            }
+            const int64_t rel = x - seq_start;
+            const int64_t item = rel / s.total;
+            const int u0 = (int)(rel % s.total);
+            const int u1 = (int)min((int64_t)s.total, u0 + (end - x));
+            float *part = nullptr;
+            if (u0 > 0 || u1 < s.total) part = parts + (size_t)(2 * blockIdx.x + (u0 > 0 ? 0 : 1)) * part_floats<D>();
+            // heads inside tiles: neighbouring CTAs then read neighbouring heads of the same pages
+            do_tile<QT, CT, D, CORE>(A, s, b, (int)(item / A.H), (int)(item % A.H), u0, u1, part, sel, smem);
+            x += u1 - u0;
+        }
+    }
+}
+
+// Joins the parts of the tiles that k_attn_few split.  Grid: (tile numbers as in the unsplit launch, heads,
+// groups of JOIN_ROWS rows); split_grid: CTAs that k_attn_few was launched with; shift: its
+// Cfg::SHIFT.
+template <int QT, int D, bool CORE>
+__global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, const float *parts, int split_grid, float shift)
+{
+    __shared__ int64_t sums[JOIN_ROWS];
+    __shared__ int found;
+    __shared__ int64_t found_before;
+    const int G = A.Hq / A.H;
+    const int64_t x = blockIdx.x;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    int64_t total = 0;
+    // the sequence of this tile (the last whose tile numbers start at or before x), and the chunks before it
+    for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        Seq s = {};
+        if (b < A.B) s = load_seq<CORE>(A, b);
+        const bool mine = s.n > 0 && (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b) <= x;
+        if (mine) atomicMax(&found, b);
+        int64_t before;
+        const int64_t sum = block_scan(seq_cost(A, s), sums, before);
+        if (mine && found == b) found_before = total + before;
+        total += sum;
+        __syncthreads();
+    }
+    pdl_wait();  // (before any return: this launch must not end before the one whose parts it joins)
+    const int b = found;
+    if (b < 0) return;
+    const Seq s = load_seq<CORE>(A, b);
+    const int64_t tile = x - (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b);
+    if (tile >= s.tiles) return;
+    const int h = blockIdx.y, ctas = sharing_ctas(total, split_grid);
+    const int64_t start = found_before + (tile * A.H + h) * s.total;
+    const int c0 = cta_of(total, start, ctas), c1 = cta_of(total, start + s.total - 1, ctas);
+    if (c0 == c1) return;  // written whole
+    const Tile t = make_tile<CORE>(A, s, (int)tile);
+    const int row = blockIdx.z * JOIN_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= t.rows) return;
+    constexpr size_t PF = part_floats<D>();
+    auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * PF; };
+    float M = -INFINITY;
+    for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, part(i)[row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    constexpr int PER = D / 32;
+    float acc[PER], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; e++) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = c0; i <= c1; i++) {
+        const float *p = part(i);
+        const float m = p[row], f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+        L = fmaf(p[ROWS + row], f, L);
+#pragma unroll
+        for (int e = 0; e < PER; e++) acc[e] = fmaf(p[2 * ROWS + row * D + lane + 32 * e], f, acc[e]);
+    }
+    int64_t n, pos;
+    int g;
+    tile_row<CORE>(A, s, t, row, n, pos, g);
+    const int64_t at = n * A.Hq + h * G + g;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int e = 0; e < PER; e++) store_elem<QT>(A.out, at * D + lane + 32 * e, acc[e] * inv);
+    if (A.lse && lane == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - shift + log2f(L)) * 0.6931471805599453f;
+}
+
+// Addresses of the rows of every token's Top-k entries (0: none), for CORE.
+__global__ void __launch_bounds__(128) k_attn_entries(const AttnArgs A, const uint8_t **sel)
+{
+    __shared__ int slot;
+    pdl_trigger();
+    const int64_t n = blockIdx.x;
+    const int b = block_seq_of_token(A.q_offsets, A.B, A.N, n, &slot);
+    if (b >= A.B) return;
+    const int j = blockIdx.y * 128 + threadIdx.x;
+    if (j >= A.k) return;
+    const int32_t e = __ldg(A.topk_idx + n * A.k + j);
+    sel[n * A.k + j] = e < 0 ? nullptr : entry_row(A, b, e);
+}
+
+// CTAs of a launch that is split over keys, and the parts they may leave.
+constexpr int SPLIT_CTAS = 3 * 148;
+inline size_t parts_bytes(int D) { return (size_t)2 * SPLIT_CTAS * (2 * ROWS + (size_t)ROWS * D) * sizeof(float); }
+
+// Tiles with at most this many chunks are not split over CTAs.
+constexpr int64_t WHOLE_CHUNKS = 48;
+
+template <int QT, int CT, int D, bool CORE>
+cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st, int *launches)
+{
+    using C = Cfg<CT, D>;
+    float *parts = (float *)workspace;
+    const uint8_t **sel = (const uint8_t **)((char *)workspace + parts_bytes(D));
+    const int G = A.Hq / A.H, tpt = (G + ROWS - 1) / ROWS;
+    const int64_t tiles = CORE ? A.N * tpt : A.N * G / ROWS + A.B;
+    if (tiles >= (int64_t)1 << 31 || A.H > 65535) return cudaErrorInvalidConfiguration;
+    // chunks of a tile at most, were the tokens shared evenly by the sequences
+    const int64_t limit = (int64_t)A.max_pages * A.page;
+    const int64_t seen = A.window > 0 && A.window + A.N / A.B < limit ? A.window + A.N / A.B : limit;
+    const int64_t chunks = seen / KEYS + 2 + (A.window > 0 ? (A.n_sink < limit ? A.n_sink : limit) / KEYS + 1 : 0) + (CORE ? A.k / KEYS + 1 : 0);
+    cudaLaunchAttribute attr[1];
+    if constexpr (CORE) {
+        k_attn_entries<<<dim3((unsigned)A.N, (unsigned)((A.k + 127) / 128)), 128, 0, st>>>(A, sel);
+        ++*launches;
+    }
+    cudaError_t e;
+    if (chunks <= WHOLE_CHUNKS) {
+        auto kernel = k_attn_few<QT, CT, D, CORE, false>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H), dim3(32 * WARPS), C::SMEM, st, attr);
+        if (!CORE) cfg.numAttrs = 0;
+        e = cudaLaunchKernelEx(&cfg, kernel, A, parts, (const uint8_t *const *)sel);
+        ++*launches;
+        return e;
+    }
+    auto kernel = k_attn_few<QT, CT, D, CORE, true>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int per_sm = C::SMEM <= 74 * 1024 ? 3 : (C::SMEM <= 112 * 1024 ? 2 : 1);
+    const int grid = per_sm * sms < SPLIT_CTAS ? per_sm * sms : SPLIT_CTAS;
+    cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(32 * WARPS), C::SMEM, st, attr);
+    if (!CORE) cfg.numAttrs = 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, A, parts, (const uint8_t *const *)sel);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, attr);
+    e = cudaLaunchKernelEx(&cfg, k_attn_join<QT, D, CORE>, A, (const float *)parts, grid, C::SHIFT);
+    ++*launches;
+    return e;
+}
+
+template <int QT, int CT, bool CORE>
+cudaError_t launch_d(const AttnArgs &A, void *workspace, int sms, cudaStream_t st, int *launches)
+{
+    if (A.D == 32) return launch<QT, CT, 32, CORE>(A, workspace, sms, st, launches);
+    if (A.D == 64) return launch<QT, CT, 64, CORE>(A, workspace, sms, st, launches);
+    return launch<QT, CT, 128, CORE>(A, workspace, sms, st, launches);
+}
+
+}  // namespace few
+
+}  // namespace lsa

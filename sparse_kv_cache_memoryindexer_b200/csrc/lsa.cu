@@ -24,6 +24,7 @@
 #include "topk.cuh"
 #include "kv_append.cuh"
 #include "attn.cuh"
+#include "attn_few.cuh"
 #include "selftest.cuh"
 
 using namespace lsa;
@@ -1112,14 +1113,6 @@ lsa_status launch_append(AppendArgs &A, cudaStream_t st)
     return launched("append to the window cache");
 }
 
-template <int QT, int CT>
-lsa_status launch_attn_rows(const AttnArgs &A, cudaStream_t st)
-{
-    const dim3 grid((unsigned)A.N, (unsigned)((A.Hq + ATTN_ROW_WARPS - 1) / ATTN_ROW_WARPS));
-    k_attn_rows<QT, CT><<<grid, 32 * ATTN_ROW_WARPS, 0, st>>>(A);
-    return launched("attention (rows)");
-}
-
 lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void *workspace, size_t workspace_bytes,
                      size_t need, cudaStream_t st)
 {
@@ -1134,9 +1127,19 @@ lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void 
     if (!workspace || workspace_bytes < need) return fail(LSA_ERR_WORKSPACE, "%s: workspace needs %zu bytes", what, need);
     LSA_REQUIRE(aligned(workspace, 256), "%s: workspace must be 256-byte aligned", what);
     if (A.N == 0) return ok();
-    if (dt == DT_F32) LSA_TRY((launch_attn_rows<DT_F32, DT_F32>(A, st)));
-    else if (cdt == DT_BF16) LSA_TRY((launch_attn_rows<DT_BF16, DT_BF16>(A, st)));
-    else LSA_TRY((launch_attn_rows<DT_BF16, DT_FP8>(A, st)));
+    int n = 0;
+    cudaError_t e;
+    if (A.k > 0) {
+        if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, true>(A, workspace, num_sms(), st, &n);
+        else e = few::launch_d<DT_BF16, DT_BF16, true>(A, workspace, num_sms(), st, &n);
+    } else {
+        if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, false>(A, workspace, num_sms(), st, &n);
+        else if (cdt == DT_BF16) e = few::launch_d<DT_BF16, DT_BF16, false>(A, workspace, num_sms(), st, &n);
+        else e = few::launch_d<DT_BF16, DT_FP8, false>(A, workspace, num_sms(), st, &n);
+    }
+    g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
     return ok();
 }
 
@@ -1187,7 +1190,7 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
 size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D)
 {
     if (N < 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || D <= 0) return 0;
-    return 256;
+    return few::parts_bytes(D);
 }
 
 lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N,
@@ -1209,7 +1212,7 @@ lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt, c
 size_t lsa_core_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D, int k)
 {
     if (N < 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || D <= 0 || k < 0) return 0;
-    return 256;
+    return few::parts_bytes(D) + align_up((size_t)N * (size_t)k * 8, 256);
 }
 
 lsa_status lsa_core_attention(const void *q, int64_t q_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N,
