@@ -87,4 +87,89 @@ __device__ __forceinline__ const uint8_t *entry_row(const AttnArgs &A, int b, in
     return nullptr;
 }
 
+// Key and value rows of one cached token of head h, with their page's scales (false: the page is bad, flagged).
+template <int CT>
+__device__ __forceinline__ bool cached_rows(const AttnArgs &A, int b, int h, int64_t pos, const uint8_t *&k,
+                                            const uint8_t *&v, float &ks, float &vs)
+{
+    const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, pos / A.page);
+    if (page < 0) return false;
+    const int64_t ph = (int64_t)page * A.H + h;
+    const int64_t e = (ph * A.page + pos % A.page) * A.D;
+    constexpr int bytes = CT == DT_F32 ? 4 : (CT == DT_BF16 ? 2 : 1);
+    k = (const uint8_t *)A.k_cache + e * bytes;
+    v = (const uint8_t *)A.v_cache + e * bytes;
+    ks = vs = 1.f;
+    if constexpr (CT == DT_FP8) {
+        ks = __ldg(A.k_scale + ph);
+        vs = __ldg(A.v_scale + ph);
+        if (!good_scale(ks) || !good_scale(vs)) {
+            flag(ERRF_SCALE);
+            return false;
+        }
+    }
+    return true;
+}
+
+constexpr int ATTN_MAX_D = 128;
+
+// One query row (token n, head hq) by one warp, key by key in fp32: 32 keys at a time, a key per lane for the
+// scores, D / 32 dimensions per lane for the values.  The way out for rows whose tile met an infinity or NaN: a
+// matrix product carries one from a key that a row must not see into that row as 0 x inf.  Such a row comes out
+// as NaN, so a row that is not finite is done again here, over its own keys alone.
+// qs: the warp's D floats of shared memory.
+template <int QT, int CT>
+__device__ __noinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
+{
+    const int lane = threadIdx.x & 31;
+    const int h = hq / (A.Hq / A.H), D = A.D, per = D / 32;
+    for (int i = lane; i < D; i += 32) qs[i] = load_elem<QT>(A.q, n * A.q_stride + (int64_t)hq * D + i);
+    __syncwarp();
+    const Span sp = visible_span(pos, A.window, A.n_sink);
+    const int64_t total = sp.total;
+    float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
+#pragma unroll
+    for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;
+    for (int64_t t0 = 0; t0 < total; t0 += 32) {
+        const int64_t t = t0 + lane;
+        const uint8_t *kr = nullptr, *vr = nullptr;
+        float ks = 1.f, vs = 1.f;
+        bool there = false;
+        if (t < total) there = cached_rows<CT>(A, b, h, t < sp.sinks ? t : sp.lo + (t - sp.sinks), kr, vr, ks, vs);
+        float s = -INFINITY;
+        if (there) {
+            float d = 0.f;
+            for (int i = 0; i < D; i++) d += qs[i] * load_elem<CT>(kr, i);
+            s = d * (A.scale * ks);
+        }
+        float mx = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+        const float f = __expf(m - ref);
+        const float p = there ? __expf(s - ref) : 0.f;
+        l = l * f + p;
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= f;
+        const int many = (int)min((int64_t)32, total - t0);
+        for (int j = 0; j < many; j++) {
+            const float pj = __shfl_sync(0xffffffffu, p * vs, j);
+            const uint8_t *rj = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)vr, j);
+            if (!rj) continue;
+#pragma unroll
+            for (int i = 0; i < ATTN_MAX_D / 32; i++)
+                if (i < per) acc[i] += pj * load_elem<CT>(rj, lane + 32 * i);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < ATTN_MAX_D / 32; i++)
+        if (i < per) store_elem<QT>(A.out, (n * A.Hq + hq) * D + lane + 32 * i, acc[i] * inv);
+    if (A.lse && lane == 0) A.lse[n * A.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
+    __syncwarp();
+}
+
 }  // namespace lsa

@@ -25,6 +25,7 @@
 #include "kv_append.cuh"
 #include "attn.cuh"
 #include "attn_few.cuh"
+#include "attn_many.cuh"
 #include "selftest.cuh"
 
 using namespace lsa;
@@ -1133,7 +1134,12 @@ lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void 
         if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, true>(A, workspace, num_sms(), st, &n);
         else e = few::launch_d<DT_BF16, DT_BF16, true>(A, workspace, num_sms(), st, &n);
     } else {
-        if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, false>(A, workspace, num_sms(), st, &n);
+        if (many::takes(A, cdt)) {
+            if (cdt == DT_BF16) e = A.D == 64 ? many::launch<DT_BF16, 64>(A, workspace, num_sms(), st, &n)
+                                              : many::launch<DT_BF16, 128>(A, workspace, num_sms(), st, &n);
+            else e = A.D == 64 ? many::launch<DT_FP8, 64>(A, workspace, num_sms(), st, &n)
+                               : many::launch<DT_FP8, 128>(A, workspace, num_sms(), st, &n);
+        } else if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, false>(A, workspace, num_sms(), st, &n);
         else if (cdt == DT_BF16) e = few::launch_d<DT_BF16, DT_BF16, false>(A, workspace, num_sms(), st, &n);
         else e = few::launch_d<DT_BF16, DT_FP8, false>(A, workspace, num_sms(), st, &n);
     }
@@ -1190,7 +1196,7 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
 size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D)
 {
     if (N < 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || D <= 0) return 0;
-    return few::parts_bytes(D);
+    return std::max(few::parts_bytes(D), many::parts_bytes(N, B, H_q, H_kv, D));
 }
 
 lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt, const int64_t *q_offsets, int64_t N,
