@@ -119,7 +119,7 @@ constexpr int ATTN_MAX_D = 128;
 // as NaN, so a row that is not finite is done again here, over its own keys alone.
 // qs: the warp's D floats of shared memory.
 template <int QT, int CT>
-__device__ __noinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
+__device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
 {
     const int lane = threadIdx.x & 31;
     const int h = hq / (A.Hq / A.H), D = A.D, per = D / 32;
@@ -130,6 +130,7 @@ __device__ __noinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, i
     float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;
+#pragma unroll 1
     for (int64_t t0 = 0; t0 < total; t0 += 32) {
         const int64_t t = t0 + lane;
         const uint8_t *kr = nullptr, *vr = nullptr;
@@ -139,6 +140,7 @@ __device__ __noinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, i
         float s = -INFINITY;
         if (there) {
             float d = 0.f;
+#pragma unroll 4
             for (int i = 0; i < D; i++) d += qs[i] * load_elem<CT>(kr, i);
             s = d * (A.scale * ks);
         }
@@ -153,6 +155,7 @@ __device__ __noinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, i
 #pragma unroll
         for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= f;
         const int many = (int)min((int64_t)32, total - t0);
+#pragma unroll 1
         for (int j = 0; j < many; j++) {
             const float pj = __shfl_sync(0xffffffffu, p * vs, j);
             const uint8_t *rj = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)vr, j);

@@ -54,7 +54,12 @@ struct Cfg {
     static constexpr uint32_t BARS = 19;
     static constexpr uint32_t OFF_MISC = OFF_BAR + 8 * BARS;
     static constexpr uint32_t SMEM = OFF_MISC + 16 + 1024;
-    static constexpr int THREADS = CT == DT_FP8 ? 448 : 320;
+    static constexpr int THREADS = CT == DT_FP8 ? 512 : 384;
+    // registers of the softmax warpgroups, the one of producer and issuer, the decoding one: of 3 x 168 (bf16) or 4 x 128
+    static constexpr int REGS_SOFTMAX = CT == DT_FP8 ? 184 : 208;
+    static constexpr int REGS_ISSUE = CT == DT_FP8 ? 56 : 80;
+    static constexpr int REGS_DECODE = 88;
+    static_assert(CT == DT_FP8 ? 2 * REGS_SOFTMAX + REGS_ISSUE + REGS_DECODE <= 4 * 128 : 2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "");
     static constexpr uint32_t IDESC_S = CT == DT_FP8 ? tc::idesc_f16(128, BLOCK) : tc::idesc_bf16(128, BLOCK);
     static constexpr uint32_t IDESC_O = (CT == DT_FP8 ? tc::idesc_f16(128, D) : tc::idesc_bf16(128, D)) | (1u << 16);
     static constexpr float SHIFT = CT == DT_FP8 ? 7.f : 0.f;
@@ -85,6 +90,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16])
         ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(a));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+// Registers of a warpgroup: the kernel starts with 65536 / threads each; the shares below add up to no more.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -287,6 +315,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax: warpgroup t has tile t, a thread a row
+        setmaxnreg_inc<C::REGS_SOFTMAX>();
         const int t = warp >> 2, rr = tid & 127, r = t * TILE_ROWS + rr;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + (uint32_t)t * 128u, o_addr = tmem + lanes + 256u + (uint32_t)t * 128u;
@@ -299,52 +328,56 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         const int64_t t_first = j.len + (j.row0 + min(tr0, j.rows - 1)) / G, t_last = j.len + (j.row0 + max(tr1, 0)) / G;
         // (a factor of zero would make NaN of a masked -inf)
         const float f = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1e-30f) * (FP8 ? qfac[r] : 1.f);
-        float m = -INFINITY, l = 0.f;  // m: raw score times f (bf16: raw), of the maximum in use
+        const float fx = FP8 ? 1.f : f;  // from s to log2 units
+        float m = -INFINITY, l = 0.f;    // m: the maximum in use, in the units of s
         bool ok = true;
         for (int i = 0; i < nb; i++) {
             const int64_t p0 = block_pos(i0 + i);
             if (!mbar_wait_warp(s_full(t), i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const Meta *me = meta + (i & (META - 1));
-            const uint32_t live = me->live, zero = FP8 ? me->zero : 0u;
-            const bool whole = live == 0xFFu && p0 + BLOCK - 1 <= t_first &&
-                               (A.window == 0 || p0 > t_last - A.window || p0 + BLOCK <= A.n_sink);
-            // columns [0, hi] and ([lo, ..] or [0, sk)) of the block are visible to this row
-            const int hi = (int)max((int64_t)-1, min((int64_t)BLOCK, pos - p0)), lo = (int)max((int64_t)0, min((int64_t)BLOCK, mylow - p0)),
-                      sk = (int)max((int64_t)0, min((int64_t)BLOCK, (int64_t)A.n_sink - p0));
-            auto piece = [&](int pc, float (&v)[32]) {
-                tmem_ld32(s_addr + 32 * pc, v);
-                tmem_wait_ld();
-                if constexpr (FP8) {
+            const uint32_t live = me->live;
+            float s[4][32];
+#pragma unroll
+            for (int pc = 0; pc < 4; pc++) tmem_ld32(s_addr + 32 * pc, s[pc]);
+            tmem_wait_ld();
+            if constexpr (FP8) {
+#pragma unroll
+                for (int pc = 0; pc < 4; pc++)
 #pragma unroll
                     for (int gg = 0; gg < 2; gg++) {
                         const float a = f * me->ks[2 * pc + gg], b = me->lv[2 * pc + gg];
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const float2 y = fma2(make_float2(v[16 * gg + k], v[16 * gg + k + 1]), make_float2(a, a), make_float2(b, b));
-                            v[16 * gg + k] = y.x;
-                            v[16 * gg + k + 1] = y.y;
+                        for (int k = 16 * gg; k < 16 * gg + 16; k += 2) {
+                            const float2 y = fma2(make_float2(s[pc][k], s[pc][k + 1]), make_float2(a, a), make_float2(b, b));
+                            s[pc][k] = y.x;
+                            s[pc][k + 1] = y.y;
                         }
                     }
-                }
-                if (!whole) {
+            }
+            if (!(live == 0xFFu && p0 + BLOCK - 1 <= t_first &&
+                  (A.window == 0 || p0 > t_last - A.window || p0 + BLOCK <= A.n_sink))) {
+                // columns [0, hi) and ([lo, ..) or [0, sk)) of the block are visible to this row
+                const int hi = (int)max((int64_t)0, min((int64_t)BLOCK, pos + 1 - p0)),
+                          lo = (int)max((int64_t)0, min((int64_t)BLOCK, mylow - p0)),
+                          sk = (int)max((int64_t)0, min((int64_t)BLOCK, (int64_t)A.n_sink - p0));
 #pragma unroll
-                    for (int k = 0; k < 32; k++) {
-                        const int c = 32 * pc + k;
-                        const bool see = c <= hi && (c >= lo || c < sk) && (live >> (c >> 4) & 1);
-                        v[k] = see ? v[k] : -INFINITY;
-                    }
+                for (int pc = 0; pc < 4; pc++) {
+                    const uint32_t pages = ((live >> (2 * pc) & 1) ? 0xFFFFu : 0u) | ((live >> (2 * pc + 1) & 1) ? 0xFFFF0000u : 0u);
+                    const uint32_t w = first_bits(hi - 32 * pc) & (~first_bits(lo - 32 * pc) | first_bits(sk - 32 * pc)) & pages;
+#pragma unroll
+                    for (int k = 0; k < 32; k++) s[pc][k] = (w & (1u << k)) ? s[pc][k] : -INFINITY;
                 }
-            };
-            float mx = -INFINITY;
+            }
+            float mx4[4];
 #pragma unroll
             for (int pc = 0; pc < 4; pc++) {
-                float v[32];
-                piece(pc, v);
+                mx4[pc] = s[pc][0];
 #pragma unroll
-                for (int k = 0; k < 32; k++) mx = fmaxf(mx, v[k]);
+                for (int k = 1; k < 31; k += 2) mx4[pc] = fmaxf(fmaxf(mx4[pc], s[pc][k]), s[pc][k + 1]);
+                mx4[pc] = fmaxf(mx4[pc], s[pc][31]);
             }
-            const float fx = FP8 ? 1.f : f;  // from v to log2 units
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             const bool grow = m == -INFINITY ? mx != -INFINITY : (mx - m) * fx > STALE;
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = fmaxf(m, mx);
@@ -354,48 +387,43 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 if (i > 0) {
                     if (!mbar_wait_warp(o_done(t), (i - 1) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-#pragma unroll
-                    for (int pc = 0; pc < D / 32; pc++) {
-                        float v[32];
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
                         uint32_t u[16];
-                        tmem_ld32(o_addr + 32 * pc, v);
+                        tmem_ld16(o_addr + c, u);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int hf = 0; hf < 2; hf++) {
-#pragma unroll
-                            for (int k = 0; k < 16; k++) u[k] = __float_as_uint(v[16 * hf + k] * ff);
-                            tmem_st16(o_addr + 32 * pc + 16 * hf, u);
-                        }
+                        for (int k = 0; k < 16; k++) u[k] = __float_as_uint(__uint_as_float(u[k]) * ff);
+                        tmem_st16(o_addr + c, u);
                     }
                     tmem_wait_st();
                 }
             }
             const float ref = (m == -INFINITY ? 0.f : m) * fx - C::SHIFT;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int pc = 0; pc < 4; pc++) {
-                float v[32];
-                piece(pc, v);
                 uint32_t u[16];
 #pragma unroll
                 for (int gg = 0; gg < 2; gg++) {
-                    float2 sum = make_float2(0.f, 0.f);
+                    if (FP8) sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
-                        float2 y = fma2(make_float2(v[16 * gg + k], v[16 * gg + k + 1]), make_float2(fx, fx), make_float2(-ref, -ref));
+                        float2 y = fma2(make_float2(s[pc][16 * gg + k], s[pc][16 * gg + k + 1]), make_float2(fx, fx), make_float2(-ref, -ref));
                         y.x = few::exp2_fast(y.x);
                         y.y = few::exp2_fast(y.y);
-                        sum.x += y.x;
-                        sum.y += y.y;
+                        sum = add2(sum, y);
                         u[8 * gg + k / 2] = FP8 ? few::pack_f16x2(y.x, y.y) : few::pack_b16x2(y.x, y.y);
                     }
-                    l = FP8 ? fmaf(sum.x + sum.y, me->inv[2 * pc + gg], l) : l + (sum.x + sum.y);
-                    if (FP8 && (zero >> (2 * pc + gg) & 1)) {
+                    if (FP8) l = fmaf(sum.x + sum.y, me->inv[2 * pc + gg], l);
+                }
+                if (FP8 && me->zero) {
 #pragma unroll
-                        for (int k = 0; k < 8; k++) u[8 * gg + k] = 0u;
-                    }
+                    for (int k = 0; k < 16; k++) u[k] = (me->zero >> (2 * pc + (k >> 3)) & 1) ? 0u : u[k];
                 }
                 tmem_st16(s_addr + 16 * pc, u);
             }
+            if (!FP8) l += sum.x + sum.y;
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full(t));
@@ -449,7 +477,9 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 attend_row<DT_BF16, CT>(A, j.b, pos2, n2, h * G + g2, (float *)(base + C::OFF_Q + t * C::TILE_BYTES) + (warp & 3) * ATTN_MAX_D);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp < 12) {
+        setmaxnreg_dec<C::REGS_ISSUE>();
+        if (warp == 8) {
         // ------------------------------------------------------- producer: lane x has page x of the block
         const int per_block = BLOCK / A.page;
         const uint32_t page_bytes = (uint32_t)A.page * (FP8 ? D : 128);  // of one box
@@ -575,7 +605,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             if (!FP8 && special) wait_alone(landed, specials & 1);
         }
         __syncwarp();
-    } else if (warp == 9) {
+        } else if (warp == 9) {
         // ------------------------------------------------------- MMA issuer
         bool ok = true;
         auto score = [&](int t, int i) {
@@ -627,10 +657,12 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             }
             __syncwarp();
         }
+        }
     } else {
-        // ------------------------------------------------------- E4M3 pages to f16 tiles (warps 10 .. 13)
+        // ------------------------------------------------------- E4M3 pages to f16 tiles (warps 12 .. 15)
         if constexpr (FP8) {
-            const int ct = tid - 320;
+            setmaxnreg_dec<C::REGS_DECODE>();
+            const int ct = tid - 384;
             constexpr int PER = D / 16;  // 16-code pieces of a row
             auto convert = [&](uint32_t raw, uint32_t tile, uint32_t live, int gap0, int gap1, int end) {
 #pragma unroll 4
