@@ -51,7 +51,7 @@ struct Cfg {
     static constexpr uint32_t OFF_META = OFF_VRAW + RAW;  // META x 112 bytes
     static constexpr uint32_t OFF_QF = OFF_META + META * 112;  // row factors [256] (E4M3)
     static constexpr uint32_t OFF_BAR = OFF_QF + (CT == DT_FP8 ? CTA_ROWS * 4 : 0);
-    static constexpr uint32_t BARS = 19;
+    static constexpr uint32_t BARS = 21;
     static constexpr uint32_t OFF_MISC = OFF_BAR + 8 * BARS;
     static constexpr uint32_t SMEM = OFF_MISC + 16 + 1024;
     static constexpr int THREADS = CT == DT_FP8 ? 512 : 384;
@@ -97,6 +97,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16])
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(a));
 }
+using tc::fma2;
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
     float2 d;
@@ -192,6 +193,34 @@ __device__ __forceinline__ void row_of(const AttnArgs &A, const Job &j, int r, i
 template <int D>
 constexpr size_t part_floats() { return 2 * CTA_ROWS + (size_t)CTA_ROWS * D; }
 
+// Bounded waits as tc::mbar_wait and tc::mbar_wait_warp, for barriers that complete every microsecond: the clock
+// is read once in 64 tries (each of which the hardware may hold for a while), since reading %globaltimer takes
+// longer than most waits here.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (tc::mbar_try(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; i++) {
+        if (tc::mbar_try(bar, parity)) return true;
+        if ((i & 63) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = tc::gtime();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > tc::WAIT_NS) {
+                *abort_flag = 1;
+                flag(ERRF_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+// The whole warp waits: every lane polls (one instruction for all of them), and they leave together.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    const bool ok = wait_bar(bar, parity, abort_flag);
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity)
 {
     volatile int never = 0;
@@ -225,6 +254,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
     auto o_done = [&](int t) { return bar(12 + t); };
     const uint32_t landed = bar(14), kraw_full = bar(14), kraw_empty = bar(15), vraw_full = bar(16), vraw_empty = bar(17),
                    drained = bar(18);
+    auto p_half = [&](int t) { return bar(19 + t); };
 
     // later tiles first: with no window they have the most keys
     const int64_t x = (int64_t)gridDim.x - 1 - blockIdx.x;
@@ -258,6 +288,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             mbar_init(v_empty(s), 1);
             mbar_init(s_full(s), 1);
             mbar_init(p_full(s), 128);
+            mbar_init(p_half(s), 128);
             mbar_init(o_done(s), 1);
         }
         mbar_init(bar(14), 1);    // (landed, or kraw_full)
@@ -333,14 +364,16 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         bool ok = true;
         for (int i = 0; i < nb; i++) {
             const int64_t p0 = block_pos(i0 + i);
-            if (!mbar_wait_warp(s_full(t), i & 1, abort_flag)) { ok = false; break; }
+            if (!wait_warp(s_full(t), i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const Meta *me = meta + (i & (META - 1));
             const uint32_t live = me->live;
             float s[4][32];
 #pragma unroll
-            for (int pc = 0; pc < 4; pc++) tmem_ld32(s_addr + 32 * pc, s[pc]);
-            tmem_wait_ld();
+            for (int pc = 0; pc < 4; pc++) {
+                tmem_ld32(s_addr + 32 * pc, s[pc]);
+                if (pc & 1) tmem_wait_ld();
+            }
             if constexpr (FP8) {
 #pragma unroll
                 for (int pc = 0; pc < 4; pc++)
@@ -385,7 +418,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 m = mn;
                 l *= ff;
                 if (i > 0) {
-                    if (!mbar_wait_warp(o_done(t), (i - 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!wait_warp(o_done(t), (i - 1) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -422,13 +455,18 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     for (int k = 0; k < 16; k++) u[k] = (me->zero >> (2 * pc + (k >> 3)) & 1) ? 0u : u[k];
                 }
                 tmem_st16(s_addr + 16 * pc, u);
+                if (pc == 1) {  // the product over the first 64 keys can start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_half(t));
+                }
             }
             if (!FP8) l += sum.x + sum.y;
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full(t));
         }
-        if (ok && !mbar_wait_warp(o_done(t), (nb - 1) & 1, abort_flag)) ok = false;
+        if (ok && !wait_warp(o_done(t), (nb - 1) & 1, abort_flag)) ok = false;
         if (ok) {
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -508,7 +546,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             const int y = (int)(((int64_t)max(page, 0) * A.H + h) * A.page);
             // keys.  (A block's Meta is written once its stage is free, when S of block i - 2 is done: softmax may
             // still be at i - 2, or i - 3 of the E4M3 path, which runs one block further ahead, but no further back.)
-            if (!mbar_wait_warp(FP8 ? kraw_empty : k_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
+            if (!wait_warp(FP8 ? kraw_empty : k_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
             Meta *me = meta + (i & (META - 1));
             if (lane < per_block) {
                 const float lv = FP8 && page >= 0 && vs > 0.f ? log2f(vs) : 0.f, inv = FP8 && page >= 0 && vs > 0.f ? 1.f / vs : 1.f;
@@ -542,7 +580,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             }
             __syncwarp();
             // values
-            if (!mbar_wait_warp(FP8 ? vraw_empty : v_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
+            if (!wait_warp(FP8 ? vraw_empty : v_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
             const uint32_t vdst = sbase + (FP8 ? C::OFF_VRAW : C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES);
             uint32_t vf = FP8 ? vraw_full : v_full(i & 1);
             if constexpr (!FP8) {
@@ -576,7 +614,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     for (int bx = 0; bx < NB; bx++) tma_load_2d(vdst + (uint32_t)lane * page_bytes + bx * 16384u, &vmap, 64 * bx, y, vf);
                 __syncwarp();
                 if (special) {  // (a few blocks of a CTA's: at the ends of the first tokens, the window, the cache)
-                    if (!mbar_wait_warp(landed, specials & 1, abort_flag)) break;
+                    if (!wait_warp(landed, specials & 1, abort_flag)) break;
                     clear(true);
                     if (lane == 0) mbar_arrive(real);
                     __syncwarp();
@@ -606,10 +644,11 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         }
         __syncwarp();
         } else if (warp == 9) {
-        // ------------------------------------------------------- MMA issuer
-        bool ok = true;
-        auto score = [&](int t, int i) {
-            if (elect_one()) {
+        // ------------------------------------------------------- MMA issuer: one thread from here to the end (the
+        // tensor core waits for it; warp-wide waits and elections cost it about 100 clocks each)
+        if (elect_one()) {
+            bool ok = true;
+            auto score = [&](int t, int i) {
                 const uint32_t q = sbase + C::OFF_Q + (uint32_t)t * C::TILE_BYTES, k = sbase + C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk++) {
@@ -618,45 +657,48 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 }
                 mma_commit(s_full(t));
                 if (t == 1) mma_commit(k_empty(i & 1));
-            }
-            __syncwarp();
-        };
-        auto value = [&](int t, int i) {
-            if (elect_one()) {
+            };
+            auto value = [&](int t, int i, int half) {
                 const uint32_t v = sbase + C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES;
 #pragma unroll
-                for (int kk = 0; kk < BLOCK / 16; kk++)
+                for (int k2 = 0; k2 < BLOCK / 32; k2++) {
+                    const int kk = half * (BLOCK / 32) + k2;
                     mma_ts(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + 8u * kk,
                            train_tc::sdesc_mn(v + 2048u * kk, 16384u, 1024u), C::IDESC_O, (i > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(o_done(t));
-                if (t == 1) mma_commit(v_empty(i & 1));
-            }
-            __syncwarp();
-        };
-        if (!mbar_wait_warp(k_full(0), 0, abort_flag)) ok = false;
-        if (ok) {
-            tc_fence_after();
-            score(0, 0);
-            score(1, 0);
-        }
-        for (int i = 0; i < nb && ok; i++) {
-            if (!mbar_wait_warp(v_full(i & 1), (i >> 1) & 1, abort_flag)) { ok = false; break; }
-            if (i + 1 < nb && !mbar_wait_warp(k_full((i + 1) & 1), ((i + 1) >> 1) & 1, abort_flag)) { ok = false; break; }
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-                if (!mbar_wait_warp(p_full(t), i & 1, abort_flag)) { ok = false; break; }
+                }
+                if (half == 1) {
+                    mma_commit(o_done(t));
+                    if (t == 1) mma_commit(v_empty(i & 1));
+                }
+            };
+            ok = wait_bar(k_full(0), 0, abort_flag);
+            if (ok) {
                 tc_fence_after();
-                value(t, i);
-                if (i + 1 < nb) score(t, i + 1);
+                score(0, 0);
+                score(1, 0);
             }
-        }
-        if (!ok) {  // whatever was issued ends before TMEM and shared memory go
-            if (elect_one()) {
+            for (int i = 0; i < nb && ok; i++) {
+                const bool more = i + 1 < nb;
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    ok = wait_bar(p_half(t), i & 1, abort_flag) && (t == 1 || wait_bar(v_full(i & 1), (i >> 1) & 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    value(t, i, 0);
+                    ok = wait_bar(p_full(t), i & 1, abort_flag) &&
+                         (t == 1 || !more || wait_bar(k_full((i + 1) & 1), ((i + 1) >> 1) & 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    value(t, i, 1);
+                    if (more) score(t, i + 1);
+                }
+            }
+            if (!ok) {  // whatever was issued ends before TMEM and shared memory go
                 mma_commit(drained);
                 wait_alone(drained, 0);
             }
-            __syncwarp();
         }
+        __syncwarp();
         }
     } else {
         // ------------------------------------------------------- E4M3 pages to f16 tiles (warps 12 .. 15)
@@ -687,15 +729,15 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 const int64_t p0 = block_pos(i0 + i);
                 int gap0, gap1, end;
                 seen_rows(A, j, p0, gap0, gap1, end);
-                if (!mbar_wait_warp(kraw_full, i & 1, abort_flag)) break;
+                if (!wait_warp(kraw_full, i & 1, abort_flag)) break;
                 const uint32_t live = meta[i & (META - 1)].live;
-                if (!mbar_wait_warp(k_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
+                if (!wait_warp(k_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
                 convert(C::OFF_KRAW, C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES, live, gap0, gap1, end);
                 fence_async();
                 mbar_arrive(k_full(i & 1));
                 mbar_arrive(kraw_empty);
-                if (!mbar_wait_warp(vraw_full, i & 1, abort_flag)) break;
-                if (!mbar_wait_warp(v_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
+                if (!wait_warp(vraw_full, i & 1, abort_flag)) break;
+                if (!wait_warp(v_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
                 convert(C::OFF_VRAW, C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES, live, gap0, gap1, end);
                 fence_async();
                 mbar_arrive(v_full(i & 1));
