@@ -26,7 +26,7 @@ struct AttnArgs {
     void *out;                 // [N][Hq][D]
     float *lse;                // [N][Hq] or null
     int64_t N, n_pages;
-    int B, max_pages, Hq, H, D, page, window, n_sink;
+    int B, max_pages, Hq, H, D, page, page_shift, window, n_sink;
     float scale;
     // the Top-k entries of each query token (k = 0: none)
     const int32_t *topk_idx;   // [N][k]

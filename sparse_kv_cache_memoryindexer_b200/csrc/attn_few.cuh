@@ -44,7 +44,7 @@ struct Cfg {
     static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
     static constexpr int NT = D / 8;                // n-tiles of the value product
     static constexpr int QREGS = CT == DT_F32 ? D / 2 : D / 4;  // query fragment registers
-    static constexpr int SMEM = RING + WARPS * (ROWS * KEYS * 4) + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 16;
+    static constexpr int SMEM = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 16;
 };
 
 // 16-byte piece of a row that holds piece c of row `row`: chosen for each access pattern below so that the
@@ -56,15 +56,6 @@ __device__ __forceinline__ int swz(int row, int c)
     else if constexpr (CT == DT_F32 || D == 128) return c ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2));
     else if constexpr (D == 64) return c ^ (((row >> 1) & 1) << 1);
     else return c;
-}
-
-// Byte offset of element i of row `row` in a swizzled chunk.
-template <int CT, int D>
-__device__ __forceinline__ uint32_t elem_off(int row, int i)
-{
-    using C = Cfg<CT, D>;
-    const int byte = i * C::EB;
-    return (uint32_t)(row * C::RB + swz<CT, D>(row, byte >> 4) * 16 + (byte & 15));
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -142,6 +133,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ bool finite4(const float4 &v)
+{
+    return fabsf(v.x) <= 3.4028235e38f && fabsf(v.y) <= 3.4028235e38f && fabsf(v.z) <= 3.4028235e38f && fabsf(v.w) <= 3.4028235e38f;
+}
 
 // Two E4M3 codes to two f16 (exact; a NaN code stays NaN).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes)
@@ -347,70 +343,13 @@ __device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], floa
     }
 }
 
-template <int CT, int D>
-__device__ __forceinline__ float smem_elem(const uint8_t *chunk, int row, int i)
-{
-    const uint8_t *p = chunk + elem_off<CT, D>(row, i);
-    if constexpr (CT == DT_F32) return *(const float *)p;
-    else if constexpr (CT == DT_BF16) return bf16_bits_to_float(*(const uint16_t *)p);
-    else return e4m3_to_float(*p);
-}
-
-// Whether a chunk of values holds an infinity or NaN (the whole warp asks).
-template <int CT, int D>
-__device__ __forceinline__ bool any_nonfinite(uint32_t vb)
-{
-    bool bad = false;
-#pragma unroll 1
-    for (int i = threadIdx.x & 31; i < Cfg<CT, D>::RB; i += 32) {
-        const uint4 v = lds128(vb + (uint32_t)i * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int t = 0; t < 4; t++) {
-            if constexpr (CT == DT_F32) bad |= (w[t] & 0x7F800000u) == 0x7F800000u;
-            else if constexpr (CT == DT_BF16)
-                bad |= (w[t] & 0x7F80u) == 0x7F80u || (w[t] & 0x7F800000u) == 0x7F800000u;
-            else
-                bad |= __vcmpeq4(w[t] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
-        }
-    }
-    return __any_sync(0xffffffffu, bad);
-}
-
-// acc += p . values key by key, skipping a row's masked keys (p = 0): for a chunk in which a key that some rows
-// must not see holds an infinity or NaN, which a matrix product would carry into them as 0 x inf.
-template <int CT, int D>
-__device__ __noinline__ void values_by_key(const uint8_t *chunk, float *ps, const float (&p)[2][4], float (&acc)[Cfg<CT, D>::NT][4])
-{
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int j = 0; j < 2; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) ps[(r + 8 * (e >> 1)) * KEYS + 8 * j + 2 * c + (e & 1)] = p[j][e];
-    __syncwarp();
-#pragma unroll 1
-    for (int k = 0; k < KEYS; k++) {
-        const float p0 = ps[r * KEYS + k], p1 = ps[(r + 8) * KEYS + k];
-#pragma unroll
-        for (int t = 0; t < Cfg<CT, D>::NT; t++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float v = smem_elem<CT, D>(chunk, k, out_dim<CT>(t, c, e));
-                if (p0 != 0.f) acc[t][e] += p0 * v;
-                if (p1 != 0.f) acc[t][2 + e] += p1 * v;
-            }
-    }
-    __syncwarp();
-}
-
 // --------------------------------------------------------------------------------------- the work
 
 // What the tiles of one sequence share.  Chunks are numbered [first tokens][window]: chunk u < sc is positions
 // 16 u .., the others 16 (wc0 + u - sc) .., up to `chunks`; then the chunks of the Top-k list.
 struct Seq {
-    int64_t off;    // first query token
-    int64_t n;      // query tokens
-    int64_t len;    // tokens before this call's
+    int off, n;     // first query token, query tokens
+    int len;        // tokens before this call's
     int tiles;      // tiles of 16 rows
     int sc, wc0;
     int chunks;     // of the cache
@@ -428,38 +367,35 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &A, int b)
         flag(ERRF_OFFSETS);
         return s;
     }
-    s.off = lo;
-    s.n = hi - lo;
-    s.len = __ldg(A.cache_len + b);
+    s.off = (int)lo;
+    s.n = (int)(hi - lo);
     if (s.n == 0) return s;
+    s.len = __ldg(A.cache_len + b);
     const int G = A.Hq / A.H;
-    s.tiles = CORE ? (int)s.n * tiles_per_token(A) : (int)((s.n * G + ROWS - 1) / ROWS);
+    s.tiles = CORE ? s.n * tiles_per_token(A) : (int)(((int64_t)s.n * G + ROWS - 1) / ROWS);
+    const int limit = A.max_pages << A.page_shift;  // (below 2^31)
     if (s.len < 0) {
         flag(ERRF_COUNT);
         s.len = -s.n;  // every query stands before position 0: nothing to see
-    }
-    const int64_t limit = (int64_t)A.max_pages * A.page;
-    int64_t last = s.len + s.n - 1;
-    if (last >= limit) {
+    } else if ((int64_t)s.len + s.n > limit) {
         flag(ERRF_COUNT);
-        last = limit - 1;
+        s.len = min(s.len, 0x7FFFFFFF - (1 << 25));  // (positions stay in 32 bits)
     }
-    const Span first = visible_span(s.len < 0 ? 0 : s.len, A.window, A.n_sink);
+    const int last = min(s.len + s.n, limit) - 1;
+    const Span first = visible_span(max(s.len, 0), A.window, A.n_sink);
     s.wc0 = (int)(first.lo / KEYS);
-    const int sink_chunks = (int)((first.sinks + KEYS - 1) / KEYS);
-    s.sc = sink_chunks < s.wc0 ? sink_chunks : s.wc0;
-    const int64_t wend = last < 0 ? 0 : last / KEYS + 1;
-    s.chunks = s.sc + (wend > s.wc0 ? (int)(wend - s.wc0) : 0);
-    if (s.sc > limit / KEYS) s.sc = s.chunks = (int)(limit / KEYS);
-    s.total = s.chunks + (CORE ? (A.k + KEYS - 1) / KEYS : 0);
-    if (s.total < 1) s.total = 1;  // a tile without keys still writes its rows
+    s.sc = min((int)((first.sinks + KEYS - 1) / KEYS), s.wc0);
+    const int wend = last < 0 ? 0 : last / KEYS + 1;
+    s.sc = min(s.sc, limit / KEYS);
+    s.chunks = s.sc + max(0, wend - s.wc0);
+    s.total = max(1, s.chunks + (CORE ? (A.k + KEYS - 1) / KEYS : 0));  // (a tile without keys still writes its rows)
     return s;
 }
 
 // One tile: 16 rows of a sequence and head.
 struct Tile {
-    int64_t n0;      // CORE: its token; else the sequence's first token
-    int64_t p_lo, p_hi;  // positions of its first and last row's tokens
+    int n0;          // CORE: its token; else the sequence's first token
+    int p_lo, p_hi;  // positions of its first and last row's tokens
     int row0;        // first row (token-major within the sequence; CORE: first head of the group)
     int rows;
 };
@@ -478,7 +414,7 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &A, const Seq &s, int t
     } else {
         t.n0 = s.off;
         t.row0 = tile * ROWS;
-        t.rows = (int)min((int64_t)ROWS, s.n * G - t.row0);
+        t.rows = (int)min((int64_t)ROWS, (int64_t)s.n * G - t.row0);
         t.p_lo = s.len + t.row0 / G;
         t.p_hi = s.len + (t.row0 + t.rows - 1) / G;
     }
@@ -487,7 +423,7 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &A, const Seq &s, int t
 
 // Token of row i of the tile, its position, and its head in the group.
 template <bool CORE>
-__device__ __forceinline__ void tile_row(const AttnArgs &A, const Seq &s, const Tile &t, int i, int64_t &n, int64_t &pos, int &g)
+__device__ __forceinline__ void tile_row(const AttnArgs &A, const Seq &s, const Tile &t, int i, int &n, int &pos, int &g)
 {
     if constexpr (CORE) {
         n = t.n0;
@@ -515,32 +451,29 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + warp * C::STAGES * C::CHUNK;
     const uint32_t ring_a = (uint32_t)__cvta_generic_to_shared(ring);
-    float *ps = (float *)(smem + C::RING) + warp * ROWS * KEYS;
-    float *ml = (float *)(smem + C::RING + WARPS * ROWS * KEYS * 4);
+    float *ml = (float *)(smem + C::RING);
     struct Meta { float ks, vs; uint32_t live, pad; };
     Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
     const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
 
     const Tile t = make_tile<CORE>(A, s, tile);
     const int G = A.Hq / A.H;
-    const int64_t low = (A.window > 0 && t.p_lo + 1 > A.window) ? t.p_lo + 1 - A.window : 0;  // first window key of the first row
+    const int low = A.window > 0 ? max(0, t.p_lo + 1 - A.window) : 0;  // first window key of the first row
 
     // the chunks of this tile among [u0, u1): [u0, min(u1, sc)) and [max(u0, a), min(u1, z)), then the Top-k list's
     // (first tokens that reach into the window's chunks: none of those is skipped)
-    const int a = A.n_sink > s.wc0 * KEYS ? s.sc : max(s.sc, s.sc + (int)(low / KEYS) - s.wc0);
-    const int z = t.p_hi < 0 ? 0 : (int)min((int64_t)s.chunks, s.sc + t.p_hi / KEYS - s.wc0 + 1);
-    const int e0 = max(0, min(u1, s.sc) - u0);
-    const int b0 = max(u0, a), e1 = max(0, min(u1, z) - b0);
+    const int a = A.n_sink > s.wc0 * KEYS ? s.sc : max(s.sc, s.sc + low / KEYS - s.wc0);
+    const int z = t.p_hi < 0 ? 0 : min(s.chunks, s.sc + t.p_hi / KEYS - s.wc0 + 1);
+    const int e0 = t.p_hi < 0 ? 0 : max(0, min(u1, s.sc) - u0);
+    const int b0 = max(u0, a), e1 = t.p_hi < 0 ? 0 : max(0, min(u1, z) - b0);
     const int c0 = max(u0, s.chunks), e2 = CORE ? max(0, u1 - c0) : 0;
-    const int count = t.p_hi < 0 ? (CORE ? e2 : 0) : e0 + e1 + e2;
-    auto chunk_of = [&](int i) -> int {
-        if (t.p_hi < 0) return c0 + i;
-        return i < e0 ? u0 + i : (i < e0 + e1 ? b0 + (i - e0) : c0 + (i - e0 - e1));
-    };
+    const int count = e0 + e1 + e2;
+    auto chunk_of = [&](int i) -> int { return i < e0 ? u0 + i : (i < e0 + e1 ? b0 + (i - e0) : c0 + (i - e0 - e1)); };
+    auto pos_of = [&](int u) -> int { return (u < s.sc ? u : s.wc0 + (u - s.sc)) * KEYS; };
 
     uint32_t q[C::QREGS];
     float qf[2];
-    int64_t rpos[2];
+    int rpos[2];
     {
         const void *rows[2];
 #pragma unroll
@@ -548,8 +481,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             rows[i] = nullptr;
             rpos[i] = -1;
             if (r + 8 * i < t.rows) {
-                int64_t n;
-                int g;
+                int n, g;
                 tile_row<CORE>(A, s, t, r + 8 * i, n, rpos[i], g);
                 constexpr int qb = QT == DT_F32 ? 4 : 2;
                 rows[i] = (const uint8_t *)A.q + (n * A.q_stride + (int64_t)(h * G + g) * D) * qb;
@@ -566,62 +498,97 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
 
-    // start the loads of the warp's i-th chunk (i counts the CTA's chunks: warp w takes w, w + WARPS, ..)
-    auto issue = [&](int i, int stage) {
+    // A chunk's 16 rows are RB pieces of 16 bytes for the keys and as many for the values; piece lane + 32 x goes to
+    // lane.  The swizzle repeats every 8 rows, i.e. every REP values of x.
+    constexpr int XS = C::RB / 32, REP = C::RB >= 64 ? C::RB / 64 : 1, PR = C::RB / 16;
+    uint32_t so[REP];
+#pragma unroll
+    for (int x = 0; x < REP; x++) {
+        const int piece = lane + 32 * x, row = piece / PR;
+        so[x] = (uint32_t)(row * C::RB + swz<CT, D>(row, piece % PR) * 16);
+    }
+    auto dst = [&](int x) -> uint32_t { return so[x % REP] + (uint32_t)(x / REP) * (uint32_t)(REP * 512); };
+
+    // what the loads of the CTA's i-th chunk need from memory first: its page, or its entries' rows (a lane each)
+    auto look = [&](int i) -> unsigned long long {
+        if (i >= count) return 0ull;
+        const int u = chunk_of(i);
+        if (CORE && u >= s.chunks) {
+            const int k = (u - s.chunks) * KEYS + (lane & 15);
+            return k < A.k ? __ldg((const unsigned long long *)sel + (int64_t)t.n0 * A.k + k) : 0ull;
+        }
+        return (unsigned long long)(unsigned)__ldg(A.page_table + (int64_t)b * A.max_pages + (pos_of(u) >> A.page_shift));
+    };
+    // start the loads of the CTA's i-th chunk (warp w takes w, w + WARPS, ..)
+    auto issue = [&](int i, int stage, unsigned long long found) {
         const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
         const int u = chunk_of(i);
         if (!CORE || u < s.chunks) {
-            const int64_t p0 = (int64_t)(u < s.sc ? u : s.wc0 + (u - s.sc)) * KEYS;
-            const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, p0 / A.page);
+            const int p0 = pos_of(u);
+            int page = (int)(unsigned)found;
+            if (page < 0 || page >= A.n_pages) {
+                if (lane == 0) flag(ERRF_PAGE);
+                page = -1;
+            }
             const int64_t ph = (int64_t)max(page, 0) * A.H + h;
-            const int64_t byte = (ph * A.page + p0 % A.page) * C::RB;
+            const int64_t byte = ((ph << A.page_shift) + (p0 & ((1 << A.page_shift) - 1))) * C::RB + lane * 16;
             const uint8_t *kp = (const uint8_t *)A.k_cache + byte, *vp = (const uint8_t *)A.v_cache + byte;
+            if (page >= 0 && p0 + KEYS - 1 <= t.p_hi && (p0 >= low || p0 + KEYS <= A.n_sink)) {
 #pragma unroll
-            for (int x = 0; x < C::RB / 32; x++) {
-                const int piece = lane + 32 * x, row = piece / (C::RB / 16), pc = piece % (C::RB / 16);
-                const int64_t pos = p0 + row;
-                // keys that no row of the tile sees come in as zeros
-                const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
-                const uint32_t o = (uint32_t)(row * C::RB + swz<CT, D>(row, pc) * 16);
-                cp_async16(kb + o, see ? kp + piece * 16 : (const uint8_t *)A.k_cache, see ? 16 : 0);
-                cp_async16(vb + o, see ? vp + piece * 16 : (const uint8_t *)A.v_cache, see ? 16 : 0);
+                for (int x = 0; x < XS; x++) cp_async16(kb + dst(x), kp + 512 * x, 16);
+#pragma unroll
+                for (int x = 0; x < XS; x++) cp_async16(vb + dst(x), vp + 512 * x, 16);
+            } else {  // keys that no row of the tile sees come in as zeros
+#pragma unroll
+                for (int x = 0; x < XS; x++) {
+                    const int pos = p0 + (lane + 32 * x) / PR;
+                    const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
+                    cp_async16(kb + dst(x), see ? kp + 512 * x : (const uint8_t *)A.k_cache, see ? 16 : 0);
+                    cp_async16(vb + dst(x), see ? vp + 512 * x : (const uint8_t *)A.v_cache, see ? 16 : 0);
+                }
             }
             if constexpr (CT == DT_FP8) {
                 if (lane < 2) cp_async4(meta_a + (uint32_t)stage * 16 + lane * 4, (lane ? A.v_scale : A.k_scale) + ph, page >= 0 ? 4 : 0);
             }
             if (lane == 0) meta[stage].live = page >= 0 ? 0xFFFFu : 0u;
         } else {
-            const int j = (u - s.chunks) * KEYS + (lane & 15);
-            const uint8_t *row_p = j < A.k ? (const uint8_t *)__ldg((const unsigned long long *)sel + t.n0 * A.k + j) : nullptr;
-            const uint32_t live = __ballot_sync(0xffffffffu, row_p != nullptr) & 0xFFFFu;
+            const uint32_t live = __ballot_sync(0xffffffffu, found != 0ull) & 0xFFFFu;
 #pragma unroll
-            for (int x = 0; x < C::RB / 32; x++) {
-                const int piece = lane + 32 * x, row = piece / (C::RB / 16), pc = piece % (C::RB / 16);
-                const uint8_t *p = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)row_p, row);
-                const uint32_t o = (uint32_t)(row * C::RB + swz<CT, D>(row, pc) * 16);
-                cp_async16(kb + o, p ? p + (int64_t)h * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
-                cp_async16(vb + o, p ? p + (int64_t)(A.H + h) * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
+            for (int x = 0; x < XS; x++) {
+                const int piece = lane + 32 * x, pc = piece % PR;
+                const uint8_t *p = (const uint8_t *)__shfl_sync(0xffffffffu, found, piece / PR);
+                cp_async16(kb + dst(x), p ? p + (int64_t)h * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
+                cp_async16(vb + dst(x), p ? p + (int64_t)(A.H + h) * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
             }
             if (lane == 0) meta[stage].live = live;
         }
     };
 
+    float last_vs = 1.f, lv = 0.f, inv_vs = 1.f;
+    {
+        unsigned long long f[C::STAGES - 1];  // (the first look-ups together)
 #pragma unroll
-    for (int st = 0; st < C::STAGES - 1; st++) {
-        if (warp + st * WARPS < count) issue(warp + st * WARPS, st);
-        cp_commit();
+        for (int st = 0; st < C::STAGES - 1; st++) f[st] = look(warp + st * WARPS);
+#pragma unroll
+        for (int st = 0; st < C::STAGES - 1; st++) {
+            if (warp + st * WARPS < count) issue(warp + st * WARPS, st, f[st]);
+            cp_commit();
+        }
     }
+    unsigned long long next = look(warp + (C::STAGES - 1) * WARPS);
     int stage = 0, fill = C::STAGES - 1;
+#pragma unroll 1
     for (int i = warp; i < count; i += WARPS) {
-        if (i + (C::STAGES - 1) * WARPS < count) issue(i + (C::STAGES - 1) * WARPS, fill);
+        if (i + (C::STAGES - 1) * WARPS < count) issue(i + (C::STAGES - 1) * WARPS, fill, next);
         cp_commit();
+        next = look(i + C::STAGES * WARPS);
         cp_wait<C::STAGES - 1>();
         __syncwarp();
         const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
         const int u = chunk_of(i);
         const bool listed = CORE && u >= s.chunks;
         uint32_t live = meta[stage].live;
-        float ks = 1.f, vs = 1.f, lv = 0.f, inv_vs = 1.f;
+        float ks = 1.f, vs = 1.f;
         if constexpr (CT == DT_FP8) {
             ks = meta[stage].ks;
             vs = meta[stage].vs;
@@ -629,27 +596,28 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 if (lane == 0) flag(ERRF_SCALE);
                 live = 0;
             }
-            if (vs > 0.f) {
-                lv = log2f(vs);
-                inv_vs = 1.f / vs;
+            if (vs != last_vs) {
+                last_vs = vs;
+                lv = vs > 0.f ? log2f(vs) : 0.f;
+                inv_vs = vs > 0.f ? 1.f / vs : 1.f;
             }
         }
         float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         scores<CT, D>(kb, q, x);
-        const int64_t p0 = (int64_t)(u < s.sc ? u : s.wc0 + (u - s.sc)) * KEYS;
+        const int p0 = pos_of(u);
         const bool whole = live == 0xFFFFu &&
                            (listed || (p0 + KEYS - 1 <= t.p_lo && (A.window == 0 || p0 > t.p_hi - A.window || p0 + KEYS <= A.n_sink)));
+        const float fa = sf[0] * ks, fb = sf[1] * ks;
 #pragma unroll
         for (int j = 0; j < 2; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) x[j][e] = CT == DT_FP8 ? fmaf(x[j][e], sf[e >> 1] * ks, lv) : x[j][e] * sf[e >> 1];
+            for (int e = 0; e < 4; e++) x[j][e] = CT == DT_FP8 ? fmaf(x[j][e], e < 2 ? fa : fb, lv) : x[j][e] * (e < 2 ? fa : fb);
         if (!whole) {
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const int key = 8 * j + 2 * c + (e & 1);
-                    const int64_t pos = p0 + key, me = rpos[e >> 1];
+                    const int key = 8 * j + 2 * c + (e & 1), pos = p0 + key, me = rpos[e >> 1];
                     const bool see = (live >> key & 1) &&
                                      (listed || (pos <= me && (A.window == 0 || pos > me - A.window || pos < A.n_sink)));
                     if (!see) x[j][e] = -INFINITY;
@@ -687,25 +655,8 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 acc[i2][3] *= f[1];
             }
         }
-        if (live == 0 || (CT == DT_FP8 && vs == 0.f)) {
-            // nothing to add (a value scale of zero: the keys have had their share of the softmax sum)
-        } else if (!CORE && !whole && t.p_lo != t.p_hi && any_nonfinite<CT, D>(vb)) {
-            float px[2][4], o[C::NT][4];  // (copies: the call takes addresses, acc and x stay in registers)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                px[0][e] = x[0][e];
-                px[1][e] = x[1][e];
-#pragma unroll
-                for (int nt = 0; nt < C::NT; nt++) o[nt][e] = acc[nt][e];
-            }
-            values_by_key<CT, D>(ring + stage * C::CHUNK + KEYS * C::RB, ps, px, o);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-#pragma unroll
-                for (int nt = 0; nt < C::NT; nt++) acc[nt][e] = o[nt][e];
-        } else {
-            values<CT, D>(vb, x, acc);
-        }
+        // (a value scale of zero: the keys have had their share of the softmax sum and add nothing)
+        if (live != 0 && !(CT == DT_FP8 && vs == 0.f)) values<CT, D>(vb, x, acc);
         __syncwarp();
         stage = stage + 1 == C::STAGES ? 0 : stage + 1;
         fill = fill + 1 == C::STAGES ? 0 : fill + 1;
@@ -737,6 +688,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     }
     __syncthreads();
     constexpr int GROUPS = D / 4;  // four dimensions of a row each
+    uint32_t bad = 0;              // rows of this thread's that are not finite
     for (int i = tid; i < ROWS * GROUPS; i += 32 * WARPS) {
         const int row = i / GROUPS, d = (i % GROUPS) * 4;
         if (row >= t.rows) continue;
@@ -758,20 +710,39 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             }
             *(float4 *)(part + 2 * ROWS + row * D + d) = o;
         } else {
-            int64_t n, pos;
-            int g;
+            int n, pos, g;
             tile_row<CORE>(A, s, t, row, n, pos, g);
-            const int64_t at = n * A.Hq + h * G + g;
+            const int64_t at = (int64_t)n * A.Hq + h * G + g;
             const float inv = L == 0.f ? 0.f : 1.f / L;
+            o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+            if (!finite4(o)) bad |= 1u << row;
             if constexpr (QT == DT_F32)
-                *(float4 *)((float *)A.out + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                *(float4 *)((float *)A.out + at * D + d) = o;
             else
-                *(uint2 *)((__nv_bfloat16 *)A.out + at * D + d) =
-                    make_uint2(pack_b16x2(o.x * inv, o.y * inv), pack_b16x2(o.z * inv, o.w * inv));
+                *(uint2 *)((__nv_bfloat16 *)A.out + at * D + d) = make_uint2(pack_b16x2(o.x, o.y), pack_b16x2(o.z, o.w));
             if (A.lse && d == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - C::SHIFT + log2f(L)) * 0.6931471805599453f;
         }
     }
     __syncthreads();  // the ring is free again
+    if constexpr (!CORE) {
+        // rows of several tokens: one that is not finite may have met another's key (see attend_row)
+        if (!part && t.p_lo != t.p_hi) {
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            uint32_t *rows = (uint32_t *)smem;
+            if (lane == 0) rows[warp] = bad;
+            __syncthreads();
+            bad = rows[0] | rows[1] | rows[2] | rows[3];
+            static_assert(WARPS == 4, "the line above");
+            __syncthreads();
+            for (int row = warp; row < t.rows; row += WARPS) {
+                if (!(bad >> row & 1)) continue;
+                int n, pos, g;
+                tile_row<CORE>(A, s, t, row, n, pos, g);
+                attend_row<QT, CT>(A, b, pos, n, h * G + g, (float *)smem + warp * ATTN_MAX_D);
+            }
+            __syncthreads();
+        }
+    }
 }
 
 // Sum over the block of v, and the sum over the threads before this one.
@@ -812,8 +783,11 @@ __device__ __forceinline__ int sharing_ctas(int64_t total, int grid)
     return c < 1 ? 1 : (c < grid ? (int)c : grid);
 }
 
+template <int CT, int D>
+constexpr int CTAS_PER_SM = Cfg<CT, D>::SMEM <= 74 * 1024 ? 3 : (Cfg<CT, D>::SMEM <= 112 * 1024 ? 2 : 1);
+
 template <int QT, int CT, int D, bool CORE, bool SPLIT>
-__global__ void __launch_bounds__(32 * WARPS) k_attn_few(const AttnArgs A, float *parts, const uint8_t *const *sel)
+__global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(const AttnArgs A, float *parts, const uint8_t *const *sel)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sums[WARPS];
@@ -836,7 +810,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_attn_few(const AttnArgs A, float
         const int b = found;
         if (b < 0) return;
         const Seq s = load_seq<CORE>(A, b);
-        const int64_t tile = x - (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b);
+        const int64_t tile = x - (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b);
         if (tile < s.tiles) do_tile<QT, CT, D, CORE>(A, s, b, (int)tile, blockIdx.y, 0, s.total, nullptr, sel, smem);
     } else {
         pdl_trigger();
@@ -893,7 +867,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_attn_few(const AttnArgs A, float
 // Joins the parts of the tiles that k_attn_few split.  Grid: (tile numbers as in the unsplit launch, heads,
 // groups of JOIN_ROWS rows); split_grid: CTAs that k_attn_few was launched with; shift: its
 // Cfg::SHIFT.
-template <int QT, int D, bool CORE>
+template <int QT, int CT, int D, bool CORE>
 __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, const float *parts, int split_grid, float shift)
 {
     __shared__ int64_t sums[JOIN_ROWS];
@@ -909,7 +883,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
         const int b = b0 + threadIdx.x;
         Seq s = {};
         if (b < A.B) s = load_seq<CORE>(A, b);
-        const bool mine = s.n > 0 && (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b) <= x;
+        const bool mine = s.n > 0 && (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b) <= x;
         if (mine) atomicMax(&found, b);
         int64_t before;
         const int64_t sum = block_scan(seq_cost(A, s), sums, before);
@@ -921,7 +895,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     const int b = found;
     if (b < 0) return;
     const Seq s = load_seq<CORE>(A, b);
-    const int64_t tile = x - (CORE ? s.off * tiles_per_token(A) : s.off * G / ROWS + b);
+    const int64_t tile = x - (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b);
     if (tile >= s.tiles) return;
     const int h = blockIdx.y, ctas = sharing_ctas(total, split_grid);
     const int64_t start = found_before + (tile * A.H + h) * s.total;
@@ -948,14 +922,22 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
 #pragma unroll
         for (int e = 0; e < PER; e++) acc[e] = fmaf(p[2 * ROWS + row * D + lane + 32 * e], f, acc[e]);
     }
-    int64_t n, pos;
-    int g;
+    int n, pos, g;
     tile_row<CORE>(A, s, t, row, n, pos, g);
-    const int64_t at = n * A.Hq + h * G + g;
+    const int64_t at = (int64_t)n * A.Hq + h * G + g;
     const float inv = L == 0.f ? 0.f : 1.f / L;
+    bool bad = false;
 #pragma unroll
-    for (int e = 0; e < PER; e++) store_elem<QT>(A.out, at * D + lane + 32 * e, acc[e] * inv);
+    for (int e = 0; e < PER; e++) {
+        const float v = acc[e] * inv;
+        bad |= !(fabsf(v) <= 3.4028235e38f);
+        store_elem<QT>(A.out, at * D + lane + 32 * e, v);
+    }
     if (A.lse && lane == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - shift + log2f(L)) * 0.6931471805599453f;
+    if constexpr (!CORE) {
+        __shared__ float qs[JOIN_ROWS][ATTN_MAX_D];
+        if (t.p_lo != t.p_hi && __any_sync(0xffffffffu, bad)) attend_row<QT, CT>(A, b, pos, n, h * G + g, qs[threadIdx.x >> 5]);
+    }
 }
 
 // Addresses of the rows of every token's Top-k entries (0: none), for CORE.
@@ -1011,15 +993,14 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     auto kernel = k_attn_few<QT, CT, D, CORE, true>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    const int per_sm = C::SMEM <= 74 * 1024 ? 3 : (C::SMEM <= 112 * 1024 ? 2 : 1);
-    const int grid = per_sm * sms < SPLIT_CTAS ? per_sm * sms : SPLIT_CTAS;
+    const int grid = std::min(CTAS_PER_SM<CT, D> * sms, SPLIT_CTAS);
     cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(32 * WARPS), C::SMEM, st, attr);
     if (!CORE) cfg.numAttrs = 0;
     e = cudaLaunchKernelEx(&cfg, kernel, A, parts, (const uint8_t *const *)sel);
     if (e != cudaSuccess) return e;
     ++*launches;
     cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, attr);
-    e = cudaLaunchKernelEx(&cfg, k_attn_join<QT, D, CORE>, A, (const float *)parts, grid, C::SHIFT);
+    e = cudaLaunchKernelEx(&cfg, k_attn_join<QT, CT, D, CORE>, A, (const float *)parts, grid, C::SHIFT);
     ++*launches;
     return e;
 }

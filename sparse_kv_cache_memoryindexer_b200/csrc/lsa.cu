@@ -1114,7 +1114,7 @@ lsa_status launch_append(AppendArgs &A, cudaStream_t st)
     return launched("append to the window cache");
 }
 
-lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void *workspace, size_t workspace_bytes,
+lsa_status attention(const char *what, AttnArgs &A, int dt, int cdt, void *workspace, size_t workspace_bytes,
                      size_t need, cudaStream_t st)
 {
     LSA_REQUIRE(A.q && A.q_offsets && A.cache_len && A.page_table && A.k_cache && A.v_cache && A.out,
@@ -1128,6 +1128,7 @@ lsa_status attention(const char *what, const AttnArgs &A, int dt, int cdt, void 
     if (!workspace || workspace_bytes < need) return fail(LSA_ERR_WORKSPACE, "%s: workspace needs %zu bytes", what, need);
     LSA_REQUIRE(aligned(workspace, 256), "%s: workspace must be 256-byte aligned", what);
     if (A.N == 0) return ok();
+    for (A.page_shift = 0; 1 << A.page_shift < A.page;) ++A.page_shift;
     int n = 0;
     cudaError_t e;
     if (A.k > 0) {
