@@ -58,35 +58,6 @@ __host__ __device__ __forceinline__ Span visible_span(int64_t p, int window, int
 // in fp32, so one that is not zero lies in [2^-100, 2^120].
 __device__ __forceinline__ bool good_scale(float s) { return s == 0.f || (s >= 7.8886090522101181e-31f && s <= 1.329227995784916e36f); }
 
-// Row of entry e of sequence b (null: flagged).
-__device__ __forceinline__ const uint8_t *entry_row(const AttnArgs &A, int b, int32_t e)
-{
-    const int64_t off = __ldg(A.seq_offsets + b), S = __ldg(A.seq_offsets + b + 1) - off;
-    if (off < 0 || S < 0 || off + S > A.total_S) {
-        flag(ERRF_OFFSETS);
-        return nullptr;
-    }
-    if (e >= S) {
-        if (e - S < A.W) return A.win_kv + ((int64_t)b * A.W + (e - S)) * A.row_bytes;
-        flag(ERRF_INDEX);
-        return nullptr;
-    }
-    const int32_t cnt = __ldg(A.count + b);
-    if (cnt < 0 || cnt > S) {
-        flag(ERRF_COUNT);
-        return nullptr;
-    }
-    int64_t lo = 0, hi = cnt;  // first slot whose entry is >= e
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(A.idx + off + mid) < e) lo = mid + 1;
-        else hi = mid;
-    }
-    if (lo < cnt && __ldg(A.idx + off + lo) == e) return A.hot_kv + (off + lo) * A.row_bytes;
-    flag(ERRF_INDEX);
-    return nullptr;
-}
-
 // Key and value rows of one cached token of head h, with their page's scales (false: the page is bad, flagged).
 template <int CT>
 __device__ __forceinline__ bool cached_rows(const AttnArgs &A, int b, int h, int64_t pos, const uint8_t *&k,

@@ -18,9 +18,15 @@
 //   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
 //                (the fourth, lo lo, is below 2^-22 of the product).
 //
-// Work is either one CTA per tile, or split over keys: the chunks of all tiles of all sequences form one
-// range that the CTAs share evenly (whatever the lengths), a CTA's part of a tile that it does not hold
-// whole goes to the workspace and k_attn_join adds the parts in order.  A CTA leaves at most two parts.
+// Work is shared in one of two ways.  Tiles of bounded length (a window, a Top-k list) go to a cluster of up to
+// eight CTAs each, which share its chunks and join their sums through distributed shared memory: one launch.
+// Otherwise the chunks of all tiles of all sequences form one range that the CTAs share evenly, whatever the
+// lengths; a CTA's part of a tile that it does not hold whole goes to the workspace and k_attn_join adds the parts
+// in order.  A CTA leaves at most two parts.
+//
+// The Top-k entries' rows are looked up by the CTA that reads them, before it reads: the sequence's ascending fetch
+// list (or every 2^i-th of a long one) is copied into the ring's space and searched there.  Searching it in global
+// memory, 32 unrelated addresses an instruction, took 20 us of 55 (32 tokens, 2048 of 8847 entries each).
 #pragma once
 #include "attn.cuh"
 #include "pdl.cuh"
@@ -39,7 +45,7 @@ struct Cfg {
     static constexpr int EB = CT == DT_F32 ? 4 : (CT == DT_BF16 ? 2 : 1);
     static constexpr int RB = D * EB;               // bytes of a key or value row
     static constexpr int CHUNK = 2 * KEYS * RB;     // keys, then values
-    static constexpr int STAGES = CT == DT_FP8 ? 4 : 3;
+    static constexpr int STAGES = 3;
     static constexpr int RING = WARPS * STAGES * CHUNK;
     static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
     static constexpr int NT = D / 8;                // n-tiles of the value product
@@ -137,6 +143,42 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 __device__ __forceinline__ bool finite4(const float4 &v)
 {
     return fabsf(v.x) <= 3.4028235e38f && fabsf(v.y) <= 3.4028235e38f && fabsf(v.z) <= 3.4028235e38f && fabsf(v.w) <= 3.4028235e38f;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t a, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a, uint32_t rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at_rank(a, rank)));
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, uint32_t rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at_rank(a, rank)));
+    return v;
 }
 
 // Two E4M3 codes to two f16 (exact; a NaN code stays NaN).
@@ -343,6 +385,75 @@ __device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], floa
     }
 }
 
+// Rows of the Top-k entries [first, first + many) of query token n, sequence b, into rows[0, many): a row's number in
+// hot_kv, or ~ its number in win_kv, or NO_ROW (none, or flagged).  list: `cap` words of shared memory, free for now.
+constexpr int32_t NO_ROW = INT32_MIN;
+
+__device__ __forceinline__ void find_rows(const AttnArgs &A, int b, int n, int first, int many, int32_t *rows, int32_t *list, int cap)
+{
+    constexpr int T = 32 * WARPS, M = 8;  // M entries of a thread side by side
+    const int64_t off = __ldg(A.seq_offsets + b), S = __ldg(A.seq_offsets + b + 1) - off;
+    int cnt = __ldg(A.count + b);
+    if (off < 0 || S < 0 || off + S > A.total_S) {
+        if (threadIdx.x == 0) flag(ERRF_OFFSETS);
+        for (int i = threadIdx.x; i < many; i += T) rows[i] = NO_ROW;
+        __syncthreads();
+        return;
+    }
+    if (cnt < 0 || cnt > S) {
+        if (threadIdx.x == 0) flag(ERRF_COUNT);
+        cnt = 0;
+    }
+    const int32_t *idx = A.idx + off;
+    int sh = 0;
+    while (((cnt - 1) >> sh) + 1 > cap - 4) sh++;
+    const int m = cnt > 0 ? ((cnt - 1) >> sh) + 1 : 0;
+    // (a whole list keeps its place in a 16-byte word, so that all but its ends come 16 bytes at a time)
+    if (sh == 0) list += ((uintptr_t)idx & 15) >> 2;
+    const uint32_t la = (uint32_t)__cvta_generic_to_shared(list);
+    const int head = sh == 0 ? min(m, (int)((16 - ((uintptr_t)idx & 15)) & 15) >> 2) : m, body = (m - head) >> 2;
+    for (int i = threadIdx.x; i < head; i += T) cp_async4(la + 4 * i, idx + ((int64_t)i << sh), 4);
+    for (int i = threadIdx.x; i < body; i += T) cp_async16(la + 4 * (head + 4 * i), idx + head + 4 * i, 16);
+    for (int i = head + 4 * body + threadIdx.x; i < m; i += T) cp_async4(la + 4 * i, idx + i, 4);
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    for (int i0 = threadIdx.x; i0 < many; i0 += M * T) {
+        int32_t e[M];
+        int at[M];  // last place of the list whose entry is <= e
+#pragma unroll
+        for (int x = 0; x < M; x++) {
+            const int i = i0 + x * T;
+            e[x] = i < many && first + i < A.k ? __ldg(A.topk_idx + (int64_t)n * A.k + first + i) : -1;
+            at[x] = 0;
+        }
+        for (int c = m; c > 1;) {
+            const int half = c >> 1;
+#pragma unroll
+            for (int x = 0; x < M; x++) at[x] += list[at[x] + half] <= e[x] ? half : 0;
+            c -= half;
+        }
+#pragma unroll
+        for (int x = 0; x < M; x++) {
+            int32_t row = NO_ROW;
+            if (e[x] >= S) {
+                if (e[x] - S < A.W) row = ~(int32_t)(b * A.W + (e[x] - S));
+            } else if (e[x] >= 0 && cnt > 0) {
+                int slot = at[x] << sh;
+                for (int c = min(cnt - slot, 1 << sh); c > 1;) {  // (only where the list was thinned)
+                    const int half = c >> 1;
+                    slot += __ldg(idx + slot + half) <= e[x] ? half : 0;
+                    c -= half;
+                }
+                if ((sh == 0 ? list[slot] : __ldg(idx + slot)) == e[x]) row = (int32_t)(off + slot);
+            }
+            if (row == NO_ROW && e[x] >= 0) flag(ERRF_INDEX);
+            if (i0 + x * T < many) rows[i0 + x * T] = row;
+        }
+    }
+    __syncthreads();
+}
+
 // --------------------------------------------------------------------------------------- the work
 
 // What the tiles of one sequence share.  Chunks are numbered [first tokens][window]: chunk u < sc is positions
@@ -442,10 +553,10 @@ template <int D>
 constexpr size_t part_floats() { return 2 * ROWS + (size_t)ROWS * D; }
 
 // Chunks [u0, u1) of tile `tile` and head h of sequence b, by the whole CTA.  part: where to leave the sums (null:
-// the tile is whole, the outputs are written).
-template <int QT, int CT, int D, bool CORE>
+// the outputs are written; with CLUSTER, together with the cluster's other CTAs, which have the tile's other chunks).
+template <int QT, int CT, int D, bool CORE, bool CLUSTER>
 __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, int tile, int h, int u0, int u1, float *part,
-                                        const uint8_t *const *sel, uint8_t *smem)
+                                        uint8_t *smem)
 {
     using C = Cfg<CT, D>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
@@ -455,6 +566,8 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     struct Meta { float ks, vs; uint32_t live, pad; };
     Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
     const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
+
+    int32_t *entries = (int32_t *)(smem + C::SMEM);  // CORE: rows of the part's Top-k entries
 
     const Tile t = make_tile<CORE>(A, s, tile);
     const int G = A.Hq / A.H;
@@ -510,22 +623,19 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     auto dst = [&](int x) -> uint32_t { return so[x % REP] + (uint32_t)(x / REP) * (uint32_t)(REP * 512); };
 
     // what the loads of the CTA's i-th chunk need from memory first: its page, or its entries' rows (a lane each)
-    auto look = [&](int i) -> unsigned long long {
-        if (i >= count) return 0ull;
+    auto look = [&](int i) -> int32_t {
+        if (i >= count) return -1;
         const int u = chunk_of(i);
-        if (CORE && u >= s.chunks) {
-            const int k = (u - s.chunks) * KEYS + (lane & 15);
-            return k < A.k ? __ldg((const unsigned long long *)sel + (int64_t)t.n0 * A.k + k) : 0ull;
-        }
-        return (unsigned long long)(unsigned)__ldg(A.page_table + (int64_t)b * A.max_pages + (pos_of(u) >> A.page_shift));
+        if (CORE && u >= s.chunks) return entries[(u - c0) * KEYS + (lane & 15)];
+        return __ldg(A.page_table + (int64_t)b * A.max_pages + (pos_of(u) >> A.page_shift));
     };
     // start the loads of the CTA's i-th chunk (warp w takes w, w + WARPS, ..)
-    auto issue = [&](int i, int stage, unsigned long long found) {
+    auto issue = [&](int i, int stage, int32_t found) {
         const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
         const int u = chunk_of(i);
         if (!CORE || u < s.chunks) {
             const int p0 = pos_of(u);
-            int page = (int)(unsigned)found;
+            int page = found;
             if (page < 0 || page >= A.n_pages) {
                 if (lane == 0) flag(ERRF_PAGE);
                 page = -1;
@@ -552,21 +662,27 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             }
             if (lane == 0) meta[stage].live = page >= 0 ? 0xFFFFu : 0u;
         } else {
-            const uint32_t live = __ballot_sync(0xffffffffu, found != 0ull) & 0xFFFFu;
+            const uint32_t live = __ballot_sync(0xffffffffu, found != NO_ROW) & 0xFFFFu;
 #pragma unroll
             for (int x = 0; x < XS; x++) {
                 const int piece = lane + 32 * x, pc = piece % PR;
-                const uint8_t *p = (const uint8_t *)__shfl_sync(0xffffffffu, found, piece / PR);
-                cp_async16(kb + dst(x), p ? p + (int64_t)h * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
-                cp_async16(vb + dst(x), p ? p + (int64_t)(A.H + h) * C::RB + pc * 16 : A.hot_kv, p ? 16 : 0);
+                const int32_t row = __shfl_sync(0xffffffffu, found, piece / PR);
+                const uint8_t *p = (row >= 0 ? A.hot_kv + row * A.row_bytes : A.win_kv + (int64_t)~row * A.row_bytes) +
+                                   (int64_t)h * C::RB + pc * 16;
+                const bool there = row != NO_ROW;
+                cp_async16(kb + dst(x), there ? p : A.hot_kv, there ? 16 : 0);
+                cp_async16(vb + dst(x), there ? p + (int64_t)A.H * C::RB : A.hot_kv, there ? 16 : 0);
             }
             if (lane == 0) meta[stage].live = live;
         }
     };
 
+    if constexpr (CORE) {
+        if (e2 > 0) find_rows(A, b, t.n0, (c0 - s.chunks) * KEYS, e2 * KEYS, entries, (int32_t *)smem, C::RING / 4);
+    }
     float last_vs = 1.f, lv = 0.f, inv_vs = 1.f;
     {
-        unsigned long long f[C::STAGES - 1];  // (the first look-ups together)
+        int32_t f[C::STAGES - 1];  // (the first look-ups together)
 #pragma unroll
         for (int st = 0; st < C::STAGES - 1; st++) f[st] = look(warp + st * WARPS);
 #pragma unroll
@@ -575,7 +691,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             cp_commit();
         }
     }
-    unsigned long long next = look(warp + (C::STAGES - 1) * WARPS);
+    int32_t next = look(warp + (C::STAGES - 1) * WARPS);
     int stage = 0, fill = C::STAGES - 1;
 #pragma unroll 1
     for (int i = warp; i < count; i += WARPS) {
@@ -689,6 +805,23 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     __syncthreads();
     constexpr int GROUPS = D / 4;  // four dimensions of a row each
     uint32_t bad = 0;              // rows of this thread's that are not finite
+    auto write = [&](int row, int d, float4 o, float M, float L) {
+        int n, pos, g;
+        tile_row<CORE>(A, s, t, row, n, pos, g);
+        const int64_t at = (int64_t)n * A.Hq + h * G + g;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+        if (!finite4(o)) bad |= 1u << row;
+        if constexpr (QT == DT_F32)
+            *(float4 *)((float *)A.out + at * D + d) = o;
+        else
+            *(uint2 *)((__nv_bfloat16 *)A.out + at * D + d) = make_uint2(pack_b16x2(o.x, o.y), pack_b16x2(o.z, o.w));
+        if (A.lse && d == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - C::SHIFT + log2f(L)) * 0.6931471805599453f;
+    };
+    // the CTA's own sums, for the cluster: maxima, sums, outputs (behind the warps' outputs)
+    float *own = (float *)smem + WARPS * ROWS * D;
+    static_assert(((WARPS + 1) * ROWS * D + 2 * ROWS) * 4 <= C::RING, "the joined sums fit in the ring");
+    const uint32_t ranks = CLUSTER ? cluster_size() : 1u;
     for (int i = tid; i < ROWS * GROUPS; i += 32 * WARPS) {
         const int row = i / GROUPS, d = (i % GROUPS) * 4;
         if (row >= t.rows) continue;
@@ -703,25 +836,35 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             const float4 v = *(const float4 *)((const float *)smem + (w * ROWS + row) * D + d);
             o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
         }
-        if (part) {
+        if (part || ranks > 1) {
+            float *to = part ? part : own;
             if (d == 0) {
-                part[row] = M;
-                part[ROWS + row] = L;
+                to[row] = M;
+                to[ROWS + row] = L;
             }
-            *(float4 *)(part + 2 * ROWS + row * D + d) = o;
+            *(float4 *)(to + 2 * ROWS + row * D + d) = o;
         } else {
-            int n, pos, g;
-            tile_row<CORE>(A, s, t, row, n, pos, g);
-            const int64_t at = (int64_t)n * A.Hq + h * G + g;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-            if (!finite4(o)) bad |= 1u << row;
-            if constexpr (QT == DT_F32)
-                *(float4 *)((float *)A.out + at * D + d) = o;
-            else
-                *(uint2 *)((__nv_bfloat16 *)A.out + at * D + d) = make_uint2(pack_b16x2(o.x, o.y), pack_b16x2(o.z, o.w));
-            if (A.lse && d == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - C::SHIFT + log2f(L)) * 0.6931471805599453f;
+            write(row, d, o, M, L);
         }
+    }
+    if (CLUSTER && ranks > 1) {
+        cluster_sync();
+        const uint32_t own_a = (uint32_t)__cvta_generic_to_shared(own), me = cluster_rank(), per = ROWS / ranks;
+        for (int i = tid; i < (int)per * GROUPS; i += 32 * WARPS) {
+            const int row = (int)(me * per) + i / GROUPS, d = (i % GROUPS) * 4;
+            if (row >= t.rows) continue;
+            float M = -INFINITY, L = 0.f;
+            for (uint32_t w = 0; w < ranks; w++) M = fmaxf(M, ld_cluster(own_a + row * 4, w));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t w = 0; w < ranks; w++) {
+                const float mw = ld_cluster(own_a + row * 4, w), f = mw == -INFINITY ? 0.f : exp2_fast(mw - M);
+                const float4 v = ld_cluster4(own_a + (2 * ROWS + row * D + d) * 4, w);
+                L = fmaf(ld_cluster(own_a + (ROWS + row) * 4, w), f, L);
+                o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+            }
+            write(row, d, o, M, L);
+        }
+        cluster_sync();  // (nobody leaves, or writes its ring, while the others read its sums)
     }
     __syncthreads();  // the ring is free again
     if constexpr (!CORE) {
@@ -776,7 +919,7 @@ __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) {
 __device__ __forceinline__ int cta_of(int64_t total, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
 
 // CTAs that share the work: no more than leave MIN_CHUNKS to each.
-constexpr int MIN_CHUNKS = 4 * WARPS;
+constexpr int MIN_CHUNKS = 2 * WARPS;
 __device__ __forceinline__ int sharing_ctas(int64_t total, int grid)
 {
     const int64_t c = total / MIN_CHUNKS;
@@ -787,18 +930,18 @@ template <int CT, int D>
 constexpr int CTAS_PER_SM = Cfg<CT, D>::SMEM <= 74 * 1024 ? 3 : (Cfg<CT, D>::SMEM <= 112 * 1024 ? 2 : 1);
 
 template <int QT, int CT, int D, bool CORE, bool SPLIT>
-__global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(const AttnArgs A, float *parts, const uint8_t *const *sel)
+__global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(const AttnArgs A, float *parts)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sums[WARPS];
     __shared__ int found;
     __shared__ int64_t found_before;
     if constexpr (!SPLIT) {
-        // one CTA per tile and head; tiles of sequence b are numbered from off_b G / 16 + b (CORE: off_b tiles a token),
-        // so that ranges of ragged sequences do not meet
-        if constexpr (CORE) pdl_wait();
+        // one cluster per tile and head; tiles of sequence b are numbered from off_b G / 16 + b (CORE: off_b tiles a
+        // token), so that ranges of ragged sequences do not meet
         const int G = A.Hq / A.H;
-        const int64_t x = blockIdx.x;
+        const uint32_t Z = cluster_size(), z = cluster_rank();
+        const int64_t x = blockIdx.x / Z;
         if (threadIdx.x == 0) found = -1;
         __syncthreads();
         for (int b = threadIdx.x; b < A.B; b += blockDim.x) {
@@ -808,39 +951,47 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
         }
         __syncthreads();
         const int b = found;
-        if (b < 0) return;
+        if (b < 0) return;  // (the whole cluster)
         const Seq s = load_seq<CORE>(A, b);
         const int64_t tile = x - (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b);
-        if (tile < s.tiles) do_tile<QT, CT, D, CORE>(A, s, b, (int)tile, blockIdx.y, 0, s.total, nullptr, sel, smem);
+        if (tile >= s.tiles) return;
+        const int u0 = (int)((int64_t)s.total * z / Z), u1 = (int)((int64_t)s.total * (z + 1) / Z);
+        do_tile<QT, CT, D, CORE, true>(A, s, b, (int)tile, blockIdx.y, u0, u1, nullptr, smem);
     } else {
         pdl_trigger();
-        int64_t total = 0;
+        if (threadIdx.x == 0) found = -1;
+        int64_t total = 0, mine = 0, before = 0;  // (of the last group of sequences: the only one up to 128)
         for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
             const int b = b0 + threadIdx.x;
-            int64_t before;
-            total += block_scan(b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0, sums, before);
+            mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
+            total += block_scan(mine, sums, before);
         }
-        if constexpr (CORE) pdl_wait();
         const int ctas = sharing_ctas(total, gridDim.x);
         if (total == 0 || (int)blockIdx.x >= ctas) return;
         int64_t x = range_start(total, blockIdx.x, ctas);
         const int64_t end = range_start(total, blockIdx.x + 1, ctas);
         // the sequence that holds x
-        int64_t base = 0;
-        if (threadIdx.x == 0) found = -1;
-        for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
-            const int b = b0 + threadIdx.x;
-            const int64_t mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
-            int64_t before;
-            const int64_t sum = block_scan(mine, sums, before);
-            if (mine > 0 && base + before <= x && x < base + before + mine) {
-                found = b;
-                found_before = base + before;
+        if (A.B > (int)blockDim.x) {
+            int64_t base = 0;
+            for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
+                const int b = b0 + threadIdx.x;
+                mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
+                const int64_t sum = block_scan(mine, sums, before);
+                before += base;
+                if (base + sum > x) {
+                    if (mine > 0 && before <= x && x < before + mine) {
+                        found = b;
+                        found_before = before;
+                    }
+                    break;  // (the same for every thread)
+                }
+                base += sum;
             }
-            base += sum;
-            __syncthreads();
-            if (found >= 0) break;
+        } else if (mine > 0 && before <= x && x < before + mine) {
+            found = threadIdx.x;
+            found_before = before;
         }
+        __syncthreads();
         int b = found;
         if (b < 0) return;
         int64_t seq_start = found_before;
@@ -858,7 +1009,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
             float *part = nullptr;
             if (u0 > 0 || u1 < s.total) part = parts + (size_t)(2 * blockIdx.x + (u0 > 0 ? 0 : 1)) * part_floats<D>();
             // heads inside tiles: neighbouring CTAs then read neighbouring heads of the same pages
-            do_tile<QT, CT, D, CORE>(A, s, b, (int)(item / A.H), (int)(item % A.H), u0, u1, part, sel, smem);
+            do_tile<QT, CT, D, CORE, false>(A, s, b, (int)(item / A.H), (int)(item % A.H), u0, u1, part, smem);
             x += u1 - u0;
         }
     }
@@ -940,66 +1091,65 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     }
 }
 
-// Addresses of the rows of every token's Top-k entries (0: none), for CORE.
-__global__ void __launch_bounds__(128) k_attn_entries(const AttnArgs A, const uint8_t **sel)
-{
-    __shared__ int slot;
-    pdl_trigger();
-    const int64_t n = blockIdx.x;
-    const int b = block_seq_of_token(A.q_offsets, A.B, A.N, n, &slot);
-    if (b >= A.B) return;
-    const int j = blockIdx.y * 128 + threadIdx.x;
-    if (j >= A.k) return;
-    const int32_t e = __ldg(A.topk_idx + n * A.k + j);
-    sel[n * A.k + j] = e < 0 ? nullptr : entry_row(A, b, e);
-}
-
 // CTAs of a launch that is split over keys, and the parts they may leave.
 constexpr int SPLIT_CTAS = 3 * 148;
 inline size_t parts_bytes(int D) { return (size_t)2 * SPLIT_CTAS * (2 * ROWS + (size_t)ROWS * D) * sizeof(float); }
 
-// Tiles with at most this many chunks are not split over CTAs.
-constexpr int64_t WHOLE_CHUNKS = 48;
+// Tiles of at most this many chunks go to clusters, where these are few enough to run at once.
+constexpr int64_t CLUSTER_CHUNKS = 256;
 
 template <int QT, int CT, int D, bool CORE>
 cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st, int *launches)
 {
     using C = Cfg<CT, D>;
     float *parts = (float *)workspace;
-    const uint8_t **sel = (const uint8_t **)((char *)workspace + parts_bytes(D));
     const int G = A.Hq / A.H, tpt = (G + ROWS - 1) / ROWS;
     const int64_t tiles = CORE ? A.N * tpt : A.N * G / ROWS + A.B;
-    if (tiles >= (int64_t)1 << 31 || A.H > 65535) return cudaErrorInvalidConfiguration;
-    // chunks of a tile at most, were the tokens shared evenly by the sequences
-    const int64_t limit = (int64_t)A.max_pages * A.page;
-    const int64_t seen = A.window > 0 && A.window + A.N / A.B < limit ? A.window + A.N / A.B : limit;
-    const int64_t chunks = seen / KEYS + 2 + (A.window > 0 ? (A.n_sink < limit ? A.n_sink : limit) / KEYS + 1 : 0) + (CORE ? A.k / KEYS + 1 : 0);
+    if (tiles * 8 >= (int64_t)1 << 31 || A.H > 65535) return cudaErrorInvalidConfiguration;
+    // chunks of a tile at most, and tiles, were the tokens shared evenly by the sequences
+    const int64_t limit = (int64_t)A.max_pages * A.page, n = A.N / A.B;
+    const int64_t seen = A.window > 0 && A.window + n < limit ? A.window + n : limit;
+    const int64_t list = CORE ? (A.k + KEYS - 1) / KEYS : 0;
+    const int64_t chunks = seen / KEYS + 2 + (A.window > 0 ? (A.n_sink < limit ? A.n_sink : limit) / KEYS + 1 : 0) + list;
+    const int64_t likely = CORE ? tiles : A.B * ((n * G + ROWS - 1) / ROWS > 0 ? (n * G + ROWS - 1) / ROWS : 1);
+    const size_t smem = C::SMEM + (CORE ? (size_t)list * KEYS * 4 : 0);
+    const int per_sm = std::max(1, std::min(CTAS_PER_SM<CT, D>, (int)(227 * 1024 / (smem + 1024))));
     cudaLaunchAttribute attr[1];
-    if constexpr (CORE) {
-        k_attn_entries<<<dim3((unsigned)A.N, (unsigned)((A.k + 127) / 128)), 128, 0, st>>>(A, sel);
-        ++*launches;
-    }
     cudaError_t e;
-    if (chunks <= WHOLE_CHUNKS) {
-        auto kernel = k_attn_few<QT, CT, D, CORE, false>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H), dim3(32 * WARPS), C::SMEM, st, attr);
-        if (!CORE) cfg.numAttrs = 0;
-        e = cudaLaunchKernelEx(&cfg, kernel, A, parts, (const uint8_t *const *)sel);
-        ++*launches;
-        return e;
+    if (chunks <= CLUSTER_CHUNKS) {
+        // as many CTAs a tile as leave each one chunk a warp and run at once
+        int Z = 1;
+        while (Z < 8 && 2 * Z * WARPS <= chunks + WARPS - 1 && 2 * Z * likely * A.H <= per_sm * sms) Z *= 2;
+        // (not where the last of several waves would leave more than a quarter of the CTAs' time unused)
+        const int64_t ctas = Z * likely * A.H, slots = (int64_t)per_sm * sms;
+        if (chunks <= 64 || ctas <= slots || 4 * ctas >= 3 * ((ctas + slots - 1) / slots) * slots) {
+            auto kernel = k_attn_few<QT, CT, D, CORE, false>;
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(tiles * Z), (unsigned)A.H);
+            cfg.blockDim = dim3(32 * WARPS);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = st;
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)Z;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, kernel, A, parts);
+            ++*launches;
+            return e;
+        }
     }
     auto kernel = k_attn_few<QT, CT, D, CORE, true>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = std::min(CTAS_PER_SM<CT, D> * sms, SPLIT_CTAS);
-    cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(32 * WARPS), C::SMEM, st, attr);
-    if (!CORE) cfg.numAttrs = 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, A, parts, (const uint8_t *const *)sel);
+    const int grid = std::min(per_sm * sms, SPLIT_CTAS);
+    k_attn_few<QT, CT, D, CORE, true><<<grid, 32 * WARPS, smem, st>>>(A, parts);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;
-    cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, attr);
+    cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)tiles, (unsigned)A.H, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, attr);
     e = cudaLaunchKernelEx(&cfg, k_attn_join<QT, CT, D, CORE>, A, (const float *)parts, grid, C::SHIFT);
     ++*launches;
     return e;

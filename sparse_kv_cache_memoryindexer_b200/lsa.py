@@ -415,61 +415,85 @@ def lsa_lightning_topk_step(q_step, w_step, hot_K, hot_scale, idx, count, seq_of
 
 
 # ------------------------------------------------------------------------ core attention
+# A decode step makes these calls once per layer, so the checks are written to cost little: one pass of
+# cheap conditions; what a failed one has to say is worked out after it has failed.
 
-def _same_device(what, **named):
-    """All tensors on one CUDA device, contiguous unless they are rows with a stride (q, k, v)."""
-    dev = None
-    for name, t in named.items():
+def _placed(what, tensors, strided):
+    """All tensors on one CUDA device and contiguous (those in `strided`: on it); returns the device's index.
+    tensors, strided: tuples of (name, tensor or None) pairs, the first of `strided` given."""
+    dev = -1
+    for name, t in strided:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError("device tensor expected (got a CPU tensor)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{what}: {name} is on {t.device}, the others on {dev}")
-        if not t.is_contiguous() and name not in ("q", "k", "v"):
+        if dev < 0:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the others on cuda:{dev}")
+    for name, t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError("device tensor expected (got a CPU tensor)")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the others on cuda:{dev}")
+        if not t.is_contiguous():
             raise ValueError("tensors passed to the LSA library must be contiguous")
     return dev
 
 
-def _rows(name, t, D=None):
-    """[N][heads][D] with contiguous heads; the token stride may be larger (a slice of a fused projection)."""
-    if t.dim() != 3 or (D is not None and t.shape[2] != D):
-        raise ValueError(f"{name} must be [N][heads][{D if D is not None else 'D'}], got {list(t.shape)}")
+def _rows(name, t, D):
+    """[N][heads][D] with contiguous heads; the token stride may be larger (a slice of a fused projection).
+    Returns N, heads and the stride."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N][heads][{D}], got {list(t.shape)}")
     N, h, d = t.shape
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and h > 1):
+    s0, s1, s2 = t.stride()
+    if d != D:
+        raise ValueError(f"{name} must be [N][heads][{D}], got {list(t.shape)}")
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"the heads of a token must be contiguous in {name}")
-    if N > 1 and s[0] < h * d:
+    if N <= 1:
+        return N, h, h * d
+    if s0 < h * d:
         raise ValueError(f"tokens of {name} must not overlap")
-    return s[0] if N > 1 else h * d
+    return N, h, s0
 
 
 def _cache(what, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale):
-    """Types and shapes of the window cache (include/lsa.h); returns (B, max_pages, n_pages, H_kv, page_size, D)."""
+    """Types and shapes of the window cache (include/lsa.h); returns (B, max_pages, n_pages, H_kv, page_size, D)
+    and the cache's dtype code."""
     cdt = k_cache.dtype
-    if cdt not in DTYPE_CODE:
+    code = DTYPE_CODE.get(cdt)
+    if code is None:
         raise TypeError(f"k_cache must be fp32, bf16 or float8_e4m3fn, got {cdt}")
-    _need(cdt, v_cache=v_cache)
-    _need(torch.int64, q_offsets=q_offsets)
-    _need(torch.int32, cache_len=cache_len, page_table=page_table)
-    _need(torch.float32, k_scale=k_scale, v_scale=v_scale)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    if v_cache.dtype != cdt or q_offsets.dtype != torch.int64 or cache_len.dtype != torch.int32 or page_table.dtype != torch.int32:
+        _need(cdt, v_cache=v_cache)
+        _need(torch.int64, q_offsets=q_offsets)
+        _need(torch.int32, cache_len=cache_len, page_table=page_table)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError(f"k_cache and v_cache must be [n_pages][H_kv][page_size][D], got {list(k_cache.shape)} and "
                          f"{list(v_cache.shape)}")
-    n_pages, H, page, D = k_cache.shape
+    n_pages, H, page, D = shape
     B = cache_len.numel()
     if q_offsets.numel() != B + 1:
         raise ValueError(f"q_offsets must hold B + 1 = {B + 1} prefix offsets, got {q_offsets.numel()}")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    if page_table.dim() != 2 or page_table.size(0) != B:
         raise ValueError(f"page_table must be [B][max_pages] with B = {B}, got {list(page_table.shape)}")
-    if (cdt == torch.float8_e4m3fn) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+    if k_scale is None and v_scale is None and code != LSA_FP8_E4M3:
+        pass
+    elif k_scale is None or v_scale is None or code != LSA_FP8_E4M3:
         raise ValueError(f"{what}: k_scale and v_scale are required for an E4M3 cache (and only for it)")
-    _cap(n_pages * H, k_scale=k_scale, v_scale=v_scale)
-    return B, page_table.shape[1], n_pages, H, page, D
+    else:
+        _need(torch.float32, k_scale=k_scale, v_scale=v_scale)
+        _cap(n_pages * H, k_scale=k_scale, v_scale=v_scale)
+    return B, page_table.size(1), n_pages, H, page, D, code
 
 
 def _ptr(t):
@@ -478,54 +502,71 @@ def _ptr(t):
 
 def _on(dev, stream, f, *args):
     """The C call with the tensors' device current, on `stream` (default: that device's current stream)."""
-    if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)))
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, st)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)))
+            status = f(*args, st)
+    if status:
+        _check(status)
 
 
 def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale=None, v_scale=None, inv_freq=None,
                   interleaved=False, q=None, q_out=None, stream=None):
     """Rotate the new tokens' keys (and queries) to their positions and write keys and values into the
     paged window cache (see include/lsa.h).  q, k, v [N][heads][D] may be slices of one fused projection."""
-    dev = _same_device("lsa_kv_append", k=k, v=v, q=q, q_offsets=q_offsets, cache_len=cache_len, page_table=page_table,
-                       k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, inv_freq=inv_freq, q_out=q_out)
-    B, max_pages, n_pages, H, page, D = _cache("lsa_kv_append", q_offsets, cache_len, page_table, k_cache, v_cache,
-                                               k_scale, v_scale)
+    dev = _placed("lsa_kv_append",
+                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
+                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("inv_freq", inv_freq),
+                   ("q_out", q_out)), (("k", k), ("v", v), ("q", q)))
+    B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_kv_append", q_offsets, cache_len, page_table, k_cache, v_cache,
+                                                      k_scale, v_scale)
     dt = k.dtype
-    _need(dt, v=v, q=q, q_out=q_out)
-    _need(torch.float32, inv_freq=inv_freq)
     if dt not in DTYPE_CODE:
         raise TypeError(f"k must be fp32 or bf16, got {dt}")
-    sk, sv = _rows("k", k, D), _rows("v", v, D)
-    N = k.shape[0]
-    if k.shape[1] != H or v.shape[1] != H or v.shape[0] != N:
+    if v.dtype != dt:
+        _need(dt, v=v)
+    N, Hk, sk = _rows("k", k, D)
+    Nv, Hv, sv = _rows("v", v, D)
+    if Hk != H or Hv != H or Nv != N:
         raise ValueError(f"k and v must be [N][{H}][{D}], got {list(k.shape)} and {list(v.shape)}")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out are given together")
-    Hq, sq = H, 0
+    Hq, sq, rot = H, 0, 0
     if q is not None:
-        sq, Hq = _rows("q", q, D), q.shape[1]
-        if q.shape[0] != N:
-            raise ValueError(f"q must hold N = {N} tokens, got {q.shape[0]}")
-        _cap(N * Hq * D, q_out=q_out)
+        if q.dtype != dt or q_out.dtype != dt:
+            _need(dt, q=q, q_out=q_out)
+        Nq, Hq, sq = _rows("q", q, D)
+        if Nq != N:
+            raise ValueError(f"q must hold N = {N} tokens, got {Nq}")
+        if q_out.numel() < N * Hq * D:
+            _cap(N * Hq * D, q_out=q_out)
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32:
+            _need(torch.float32, inv_freq=inv_freq)
+        rot = 2 * inv_freq.numel()
     _on(dev, stream, _lib.lsa_kv_append, _ptr(q), sq, k.data_ptr(), sk, v.data_ptr(), sv, DTYPE_CODE[dt],
-        q_offsets.data_ptr(), N, B, cache_len.data_ptr(), page_table.data_ptr(), max_pages, _ptr(inv_freq),
-        0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)), Hq, H, D, page, n_pages,
-        k_cache.data_ptr(), v_cache.data_ptr(), DTYPE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), _ptr(q_out))
+        q_offsets.data_ptr(), N, B, cache_len.data_ptr(), page_table.data_ptr(), max_pages, _ptr(inv_freq), rot,
+        1 if interleaved else 0, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode, _ptr(k_scale),
+        _ptr(v_scale), _ptr(q_out))
 
 
-def _attention_types(what, q, H, D, out, lse_out, cdt):
-    if q.dtype not in DTYPE_CODE:
+def _attention_rows(q, D, out, lse_out):
+    code = DTYPE_CODE.get(q.dtype)
+    if code is None:
         raise TypeError(f"q must be fp32 or bf16, got {q.dtype}")
-    _need(q.dtype, out=out)
-    _need(torch.float32, lse_out=lse_out)
-    stride = _rows("q", q, D)
-    N, Hq, _ = q.shape
-    _cap(N * Hq * D, out=out)
-    _cap(N * Hq, lse_out=lse_out)
-    return stride, N, Hq
+    if out.dtype != q.dtype:
+        _need(q.dtype, out=out)
+    N, Hq, stride = _rows("q", q, D)
+    if out.numel() < N * Hq * D:
+        _cap(N * Hq * D, out=out)
+    if lse_out is not None:
+        if lse_out.dtype != torch.float32:
+            _need(torch.float32, lse_out=lse_out)
+        if lse_out.numel() < N * Hq:
+            _cap(N * Hq, lse_out=lse_out)
+    return code, N, Hq, stride
 
 
 def lsa_window_attention_workspace_size(N, B, H_q, H_kv, D) -> int:
@@ -536,17 +577,17 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
                          softmax_scale=None, k_scale=None, v_scale=None, lse_out=None, stream=None):
     """Attention over the paged window cache: a sliding window of `window` tokens (0: no limit) and the
     first n_sink tokens (see include/lsa.h).  softmax_scale defaults to D ** -0.5."""
-    dev = _same_device("lsa_window_attention", q=q, q_offsets=q_offsets, cache_len=cache_len, page_table=page_table,
-                       k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=out, lse_out=lse_out,
-                       workspace=workspace)
-    B, max_pages, n_pages, H, page, D = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
-                                               v_cache, k_scale, v_scale)
-    sq, N, Hq = _attention_types("lsa_window_attention", q, H, D, out, lse_out, k_cache.dtype)
-    _on(dev, stream, _lib.lsa_window_attention, q.data_ptr(), sq, DTYPE_CODE[q.dtype], q_offsets.data_ptr(), N, B,
-        cache_len.data_ptr(), page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(),
-        v_cache.data_ptr(), DTYPE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), int(window), int(n_sink),
-        float(D ** -0.5 if softmax_scale is None else softmax_scale), out.data_ptr(), _ptr(lse_out),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    dev = _placed("lsa_window_attention",
+                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
+                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("out", out), ("lse_out", lse_out),
+                   ("workspace", workspace)), (("q", q),))
+    B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
+                                                      v_cache, k_scale, v_scale)
+    code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
+    _on(dev, stream, _lib.lsa_window_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
+        page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode,
+        _ptr(k_scale), _ptr(v_scale), window, n_sink, D ** -0.5 if softmax_scale is None else softmax_scale,
+        out.data_ptr(), _ptr(lse_out), workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def lsa_core_attention_workspace_size(N, B, H_q, H_kv, D, k) -> int:
@@ -558,38 +599,42 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
                        stream=None):
     """One softmax over each query's Top-k entries (rows of hot_kv, or of win_kv for entries compressed
     during the window) and its window of the paged cache (see include/lsa.h)."""
-    dev = _same_device("lsa_core_attention", q=q, q_offsets=q_offsets, cache_len=cache_len, page_table=page_table,
-                       k_cache=k_cache, v_cache=v_cache, topk_idx=topk_idx, idx=idx, count=count,
-                       seq_offsets=seq_offsets, hot_kv=hot_kv, win_kv=win_kv, out=out, lse_out=lse_out,
-                       workspace=workspace)
-    B, max_pages, n_pages, H, page, D = _cache("lsa_core_attention", q_offsets, cache_len, page_table, k_cache, v_cache,
-                                               None, None)
-    sq, N, Hq = _attention_types("lsa_core_attention", q, H, D, out, lse_out, k_cache.dtype)
-    if k_cache.dtype != q.dtype:
+    dev = _placed("lsa_core_attention",
+                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
+                   ("v_cache", v_cache), ("topk_idx", topk_idx), ("idx", idx), ("count", count),
+                   ("seq_offsets", seq_offsets), ("hot_kv", hot_kv), ("win_kv", win_kv), ("out", out),
+                   ("lse_out", lse_out), ("workspace", workspace)), (("q", q),))
+    B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_core_attention", q_offsets, cache_len, page_table, k_cache,
+                                                      v_cache, None, None)
+    code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
+    if ccode != code:
         raise TypeError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
-    _need(torch.int32, topk_idx=topk_idx, idx=idx, count=count)
-    _offsets(seq_offsets, B)
-    T, k = int(total_S), topk_idx.shape[-1]
+    if topk_idx.dtype != torch.int32 or idx.dtype != torch.int32 or count.dtype != torch.int32:
+        _need(torch.int32, topk_idx=topk_idx, idx=idx, count=count)
+    if seq_offsets.dtype != torch.int64 or seq_offsets.numel() != B + 1:
+        _offsets(seq_offsets, B)
+    T, k = int(total_S), topk_idx.size(-1)
     row_bytes = 2 * H * D * q.element_size()
-    _cap(N * k, topk_idx=topk_idx)
-    _cap(T, idx=idx)
-    _cap(B, count=count)
-    _cap_bytes(T * row_bytes, hot_kv=hot_kv)
+    if topk_idx.numel() < N * k or idx.numel() < T or count.numel() < B:
+        _cap(N * k, topk_idx=topk_idx)
+        _cap(T, idx=idx)
+        _cap(B, count=count)
+    if hot_kv.numel() * hot_kv.element_size() < T * row_bytes:
+        _cap_bytes(T * row_bytes, hot_kv=hot_kv)
     W = 0
     if win_kv is not None:
-        if win_kv.dim() < 2 or win_kv.shape[0] != B:
+        if win_kv.dim() < 2 or win_kv.size(0) != B:
             raise ValueError(f"win_kv must be [B][W][row_bytes] with B = {B}, got {list(win_kv.shape)}")
-        W = win_kv.shape[1]
+        W = win_kv.size(1)
         if W == 0:
             win_kv = None
-        else:
+        elif win_kv.numel() * win_kv.element_size() < B * W * row_bytes:
             _cap_bytes(B * W * row_bytes, win_kv=win_kv)
-    _on(dev, stream, _lib.lsa_core_attention, q.data_ptr(), sq, DTYPE_CODE[q.dtype], q_offsets.data_ptr(), N, B,
-        cache_len.data_ptr(), page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(),
-        v_cache.data_ptr(), int(window), int(n_sink), float(D ** -0.5 if softmax_scale is None else softmax_scale),
-        topk_idx.data_ptr(), k, idx.data_ptr(), count.data_ptr(), seq_offsets.data_ptr(), T, hot_kv.data_ptr(), row_bytes,
-        _ptr(win_kv), W, out.data_ptr(), _ptr(lse_out), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size())
+    _on(dev, stream, _lib.lsa_core_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
+        page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), window, n_sink,
+        D ** -0.5 if softmax_scale is None else softmax_scale, topk_idx.data_ptr(), k, idx.data_ptr(), count.data_ptr(),
+        seq_offsets.data_ptr(), T, hot_kv.data_ptr(), row_bytes, _ptr(win_kv), W, out.data_ptr(), _ptr(lse_out),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 # ------------------------------------------------------------------------ cold pool
