@@ -181,12 +181,11 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a, uint32_t rank)
     return v;
 }
 
-// Two E4M3 codes to two f16 (exact; a NaN code stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes)
+// Four E4M3 codes to two pairs of f16 (exact; a NaN code stays NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t r;
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
-    return r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b)
 {
@@ -309,8 +308,11 @@ __device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, 
                 const int ks = 4 * hh + t;
                 const uint32_t a[4] = {q[4 * ks], q[4 * ks + 1], q[4 * ks + 2], q[4 * ks + 3]};
 #pragma unroll
-                for (int j = 0; j < 2; j++)
-                    mma_f16(s[j], a, e4m3x2_to_f16x2(w[j][t]), e4m3x2_to_f16x2(w[j][t] >> 16));
+                for (int j = 0; j < 2; j++) {
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16x2(w[j][t], b0, b1);
+                    mma_f16(s[j], a, b0, b1);
+                }
             }
         }
     } else {
@@ -362,10 +364,13 @@ __device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], floa
             // pairs of codes (key, key + 1) for dims 0, 1 and 2, 3 of the four
             const uint32_t x0 = __byte_perm(w[0], w[1], 0x5140), x1 = __byte_perm(w[0], w[1], 0x7362);
             const uint32_t y0 = __byte_perm(w[2], w[3], 0x5140), y1 = __byte_perm(w[2], w[3], 0x7362);
-            mma_f16(acc[4 * blk], a, e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
-            mma_f16(acc[4 * blk + 1], a, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
-            mma_f16(acc[4 * blk + 2], a, e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
-            mma_f16(acc[4 * blk + 3], a, e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+            uint32_t b[8];
+            e4m3x4_to_f16x2(x0, b[0], b[2]);
+            e4m3x4_to_f16x2(y0, b[1], b[3]);
+            e4m3x4_to_f16x2(x1, b[4], b[6]);
+            e4m3x4_to_f16x2(y1, b[5], b[7]);
+#pragma unroll
+            for (int t = 0; t < 4; t++) mma_f16(acc[4 * blk + t], a, b[2 * t], b[2 * t + 1]);
         }
     } else {
 #pragma unroll

@@ -713,10 +713,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
                     if (row < end && (row < gap0 || row >= gap1) && (live >> (row >> 4) & 1)) {
                         const uint4 w = *(const uint4 *)(base + raw + (uint32_t)e * 16);
-                        lo = make_uint4(few::e4m3x2_to_f16x2(w.x), few::e4m3x2_to_f16x2(w.x >> 16), few::e4m3x2_to_f16x2(w.y),
-                                        few::e4m3x2_to_f16x2(w.y >> 16));
-                        hi = make_uint4(few::e4m3x2_to_f16x2(w.z), few::e4m3x2_to_f16x2(w.z >> 16), few::e4m3x2_to_f16x2(w.w),
-                                        few::e4m3x2_to_f16x2(w.w >> 16));
+                        few::e4m3x4_to_f16x2(w.x, lo.x, lo.y);
+                        few::e4m3x4_to_f16x2(w.y, lo.z, lo.w);
+                        few::e4m3x4_to_f16x2(w.z, hi.x, hi.y);
+                        few::e4m3x4_to_f16x2(w.w, hi.z, hi.w);
                     }
                     uint8_t *box = base + tile + (uint32_t)(c >> 2) * 16384u;
                     // the lanes of the upper box store their halves in the other order: no two on one bank
