@@ -5,9 +5,9 @@
 // and key head are rotated in pairs (x1, x2), j < R / 2, by the angle a = p inv_freq[j]:
 //     y1 = x1 cos a - x2 sin a,   y2 = x2 cos a + x1 sin a
 // (pairs (j, j + R/2), or neighbours (2j, 2j + 1)).  At positions of a million an fp32 product would
-// leave the angle off by up to 0.06: the turns p inv_freq / 2 pi are formed and reduced to [-1/2, 1/2] in
-// fp64, then rounded once to fp32 (the angle is off by at most 2e-7) for sincospif.  The rotated value
-// is rounded once to the cache's type.
+// leave the angle off by up to 0.06: the half turns p inv_freq / pi are formed and reduced to [-1, 1] in fp64;
+// sincospif takes their fp32 value, and what that left off is put back to first order.  The rotated value is rounded
+// once to the cache's type.
 //
 // An E4M3 cache holds one scale per page, head and tensor.  The scale is a power of two, so moving the
 // page's earlier codes to a larger scale is exact except where they become subnormal; the least one
@@ -34,7 +34,8 @@ struct AppendArgs {
     float *k_scale, *v_scale;       // [n_pages][H], E4M3 only
     int64_t N, n_pages;
     int B, max_pages, Hq, H, D, page, rot, interleaved;
-    int row_ctas_per_token;         // CTAs of one token's rows
+    int tokens;                     // tokens of a CTA's rows
+    int row_ctas_per_token;         // CTAs of them
     int64_t row_ctas;               // CTAs [0, row_ctas) go by token, the others by page
 };
 
@@ -87,12 +88,17 @@ __device__ __forceinline__ void store_run8(void *row, int64_t e, const float (&x
     }
 }
 
-// cos and sin of pos * inv_freq.
+// cos and sin of pos * inv_freq: of the reduced angle's fp32 value, then corrected by what that rounding left off
+// (d, to first order: d^2 is below 2^-48).
 __device__ __forceinline__ void turn(int64_t pos, float inv_freq, float &c, float &s)
 {
-    double t = (double)pos * (double)inv_freq * 0.15915494309189533577;  // 1 / 2 pi
-    t -= rint(t);
-    sincospif((float)(t + t), &s, &c);
+    double t = (double)pos * (double)inv_freq * 0.31830988618379067154;  // 1 / pi: half turns
+    t -= 2.0 * rint(0.5 * t);
+    const float h = (float)t, d = (float)(t - (double)h) * 3.14159265f;
+    float s0, c0;
+    sincospif(h, &s0, &c0);
+    s = fmaf(c0, d, s0);
+    c = fmaf(-s0, d, c0);
 }
 
 // Rotate the eight pairs of a unit: x runs a and b (halves: a[i] with b[i]; neighbours: within a, within b).
@@ -118,18 +124,35 @@ __device__ __forceinline__ void rotate_unit(bool interleaved, const float (&c)[8
     }
 }
 
-// The sequence of token n (B: none).  Every thread of the block calls it; one round of loads.
-__device__ __forceinline__ int block_seq_of_token(const int64_t *q_offsets, int B, int64_t N, int64_t n, int *slot)
+// What a CTA needs to know of a sequence.
+struct SeqOf {
+    int64_t off, n;  // first token, tokens
+    int b, len;      // b = -1: none
+};
+
+// The sequences of tokens n .. n + many - 1 (b = -1: none, a row behind the last sequence) into slots.  Every thread
+// of the block calls it; one round of loads.
+__device__ __forceinline__ void block_seqs_of_tokens(const int64_t *q_offsets, const int32_t *cache_len, int B, int64_t N, int64_t n,
+                                                     int many, SeqOf *slots)
 {
-    if (threadIdx.x == 0) *slot = B;
+    if ((int)threadIdx.x < many) slots[threadIdx.x].b = -1;
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const int64_t lo = __ldg(q_offsets + b), hi = __ldg(q_offsets + b + 1);
-        if (lo < 0 || hi < lo || hi > N) flag(ERRF_OFFSETS);
-        else if (lo <= n && n < hi) atomicMin(slot, b);
+        const int len = __ldg(cache_len + b);
+        if (lo < 0 || hi < lo || hi > N) {
+            flag(ERRF_OFFSETS);
+        } else {  // (a token has one sequence, unless the offsets overlap: then any)
+            for (int64_t i = max(lo, n); i < min(hi, n + many); i++) {
+                SeqOf &s = slots[i - n];
+                s.off = lo;
+                s.n = hi - lo;
+                s.len = len;
+                s.b = b;
+            }
+        }
     }
     __syncthreads();
-    return *slot;
 }
 
 // Page of position pos of sequence b, or -1 (flagged) where the table has none.
@@ -147,68 +170,96 @@ __device__ __forceinline__ int32_t page_of(const int32_t *page_table, int max_pa
     return p;
 }
 
-// Rows that are stored in the type they are read in (queries; keys and values of an fp32 or bf16 cache).
+constexpr int APPEND_TOKENS = 8;  // tokens a CTA takes at most
+
+// Rows that are stored in the type they are read in (queries; keys and values of an fp32 or bf16 cache): a CTA has
+// A.tokens tokens, or a part of one token's rows.  A thread's loads of BATCH units go out together: with one unit at a
+// time a chunk of 16384 tokens ran at 5.3 TB/s.
 template <int DT, bool KV>
-__device__ __forceinline__ void append_rows(const AppendArgs &A, float2 *cs, int *slot)
+__device__ __forceinline__ void append_rows(const AppendArgs &A, float2 *cs, SeqOf *slots, int32_t *pages)
 {
-    const int64_t n = blockIdx.x / A.row_ctas_per_token;
+    constexpr int BATCH = 1;
+    const int64_t n0 = (int64_t)(blockIdx.x / A.row_ctas_per_token) * A.tokens;
     const int part = blockIdx.x % A.row_ctas_per_token;
+    const int many = (int)min((int64_t)A.tokens, A.N - n0);
     const int nq = A.q ? A.Hq : 0;
     const int rows = nq + (KV ? 2 * A.H : 0);
-    const int upr = A.D / 16, units = rows * upr;
-    const int b = block_seq_of_token(A.q_offsets, A.B, A.N, n, slot);
-    if (b >= A.B) return;  // a row behind the last sequence: left as it is
-    const int64_t len = __ldg(A.cache_len + b);
-    if (len < 0) {
-        if (threadIdx.x == 0) flag(ERRF_COUNT);
-        return;
+    const int upr = A.D / 16, units = rows * upr, half = A.rot / 2;
+    block_seqs_of_tokens(A.q_offsets, A.cache_len, A.B, A.N, n0, many, slots);
+    for (int i = threadIdx.x; i < many * half; i += blockDim.x) {
+        const int t = i / half, j = i % half;
+        const SeqOf &s = slots[t];
+        float c = 0.f, sn = 0.f;
+        if (s.b >= 0 && s.len >= 0) turn(s.len + (n0 + t - s.off), __ldg(A.inv_freq + j), c, sn);
+        cs[t * half + (j & 7) * (half >> 3) + (j >> 3)] = make_float2(c, sn);  // (units next to one another: no bank twice)
     }
-    const int64_t pos = len + (n - __ldg(A.q_offsets + b));
-    for (int j = threadIdx.x; j < A.rot / 2; j += blockDim.x) {
-        float c, s;
-        turn(pos, __ldg(A.inv_freq + j), c, s);
-        cs[j] = make_float2(c, s);
-    }
-    int32_t page = -1;
-    if (KV) page = page_of(A.page_table, A.max_pages, A.n_pages, b, pos / A.page);
-    __syncthreads();
-    for (int i = part * blockDim.x + threadIdx.x; i < units; i += A.row_ctas_per_token * blockDim.x) {
-        const int row = i / upr, u = i % upr;
-        const void *src;
-        void *dst;
-        int64_t se, de;
-        bool rot = u < A.rot / 16;
-        if (row < nq) {
-            src = A.q; se = n * A.q_stride + (int64_t)row * A.D;
-            dst = A.q_out; de = (n * A.Hq + row) * A.D;
-        } else {
-            const bool is_v = row >= nq + A.H;
-            const int h = row - nq - (is_v ? A.H : 0);
-            src = is_v ? A.v : A.k;
-            se = n * (is_v ? A.v_stride : A.k_stride) + (int64_t)h * A.D;
-            dst = is_v ? A.v_cache : A.k_cache;
-            de = (((int64_t)page * A.H + h) * A.page + pos % A.page) * A.D;
-            rot = rot && !is_v;
-            if (page < 0) continue;
-        }
-        int ra, rb;
-        if (rot) unit_runs(A, u, ra, rb);
-        else { ra = u * 16; rb = ra + 8; }
-        float xa[8], xb[8];
-        load_run8<DT>(src, se + ra, xa);
-        load_run8<DT>(src, se + rb, xb);
-        if (rot) {
-            float c[8], s[8];
-#pragma unroll
-            for (int t = 0; t < 8; t++) {
-                const float2 v = cs[u * 8 + t];
-                c[t] = v.x;
-                s[t] = v.y;
+    if ((int)threadIdx.x < many) {
+        const SeqOf s = slots[threadIdx.x];
+        int32_t page = -1;
+        if (s.b >= 0) {
+            if (s.len < 0) {
+                flag(ERRF_COUNT);
+                slots[threadIdx.x].b = -1;  // (nothing of it is touched)
+            } else if (KV) {
+                page = page_of(A.page_table, A.max_pages, A.n_pages, s.b, (s.len + (n0 + threadIdx.x - s.off)) / A.page);
             }
-            rotate_unit(A.interleaved, c, s, xa, xb);
         }
-        store_run8<DT>(dst, de + ra, xa);
-        store_run8<DT>(dst, de + rb, xb);
+        pages[threadIdx.x] = page;
+    }
+    __syncthreads();
+    const int stride = A.row_ctas_per_token * blockDim.x, total = many * units;
+    for (int i0 = part * blockDim.x + threadIdx.x; i0 < total; i0 += BATCH * stride) {
+        float xa[BATCH][8], xb[BATCH][8];
+        void *dst[BATCH];
+        int ra[BATCH], rb[BATCH], turns[BATCH];  // turns: first entry of cs, or -1
+#pragma unroll
+        for (int k = 0; k < BATCH; k++) {
+            const int i = i0 + k * stride;
+            dst[k] = nullptr;
+            if (i >= total) continue;
+            const int t = i / units, row = i % units / upr, u = i % upr;
+            const SeqOf &s = slots[t];
+            if (s.b < 0) continue;  // a row behind the last sequence: left as it is
+            const int64_t n = n0 + t;
+            const void *src;
+            int64_t se, de;
+            bool rot = u < A.rot / 16;
+            if (row < nq) {
+                src = A.q; se = n * A.q_stride + (int64_t)row * A.D;
+                dst[k] = A.q_out; de = (n * A.Hq + row) * A.D;
+            } else {
+                const bool is_v = row >= nq + A.H;
+                const int h = row - nq - (is_v ? A.H : 0);
+                if (pages[t] < 0) continue;
+                src = is_v ? A.v : A.k;
+                se = n * (is_v ? A.v_stride : A.k_stride) + (int64_t)h * A.D;
+                dst[k] = is_v ? A.v_cache : A.k_cache;
+                de = (((int64_t)pages[t] * A.H + h) * A.page + (s.len + (n - s.off)) % A.page) * A.D;
+                rot = rot && !is_v;
+            }
+            turns[k] = rot ? t * half + u : -1;
+            if (rot) unit_runs(A, u, ra[k], rb[k]);
+            else { ra[k] = u * 16; rb[k] = ra[k] + 8; }
+            load_run8<DT>(src, se + ra[k], xa[k]);
+            load_run8<DT>(src, se + rb[k], xb[k]);
+            dst[k] = (char *)dst[k] + de * (DT == DT_F32 ? 4 : 2);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; k++) {
+            if (!dst[k]) continue;
+            if (turns[k] >= 0) {
+                float c[8], s[8];
+#pragma unroll
+                for (int t = 0; t < 8; t++) {
+                    const float2 v = cs[turns[k] + t * (half >> 3)];
+                    c[t] = v.x;
+                    s[t] = v.y;
+                }
+                rotate_unit(A.interleaved, c, s, xa[k], xb[k]);
+            }
+            store_run8<DT>(dst[k], ra[k], xa[k]);
+            store_run8<DT>(dst[k], rb[k], xb[k]);
+        }
     }
 }
 
@@ -227,39 +278,48 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return lo | (hi << 16);
 }
 
-constexpr int APPEND_PAGE_THREADS = 256;
-constexpr int APPEND_PAGE_UNITS = 4;  // units of a thread: 128 tokens x 128 dimensions / 16 / 256
+constexpr int APPEND_THREADS = 256;
 
-// One page and head of an E4M3 cache, keys or values.
-template <int DT>
-__device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, int *slot, float *red)
+// One page and head of an E4M3 cache, keys or values; U units of 16 elements a thread.
+template <int DT, int U>
+__device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, SeqOf *slot, int *last, float *red)
 {
     const int tensor = (int)(job % 2);
     const int h = (int)((job / 2) % A.H);
     const int64_t pj = job / 2 / A.H;
     // Page jobs of sequence b are numbered from off_b / page + 2b: a sequence of n tokens touches at
     // most n / page + 2 pages, so the ranges do not meet.  Largest b whose range starts at or before pj.
-    if (threadIdx.x == 0) *slot = -1;
+    if (threadIdx.x == 0) *last = -1;
     __syncthreads();
+    SeqOf mine = {};
+    mine.b = -1;
     for (int b = threadIdx.x; b < A.B; b += blockDim.x) {
         const int64_t lo = __ldg(A.q_offsets + b), hi = __ldg(A.q_offsets + b + 1);
-        if (lo < 0 || hi < lo || hi > A.N) flag(ERRF_OFFSETS);
-        else if (lo / A.page + 2 * (int64_t)b <= pj) atomicMax(slot, b);
+        const int len = __ldg(A.cache_len + b);
+        if (lo < 0 || hi < lo || hi > A.N) {
+            flag(ERRF_OFFSETS);
+        } else if (lo / A.page + 2 * (int64_t)b <= pj) {
+            mine.off = lo;
+            mine.n = hi - lo;
+            mine.len = len;
+            mine.b = b;
+        }
     }
+    if (mine.b >= 0) atomicMax(last, mine.b);
     __syncthreads();
-    const int b = *slot;
-    if (b < 0) return;
-    const int64_t off = __ldg(A.q_offsets + b);
-    const int64_t n = __ldg(A.q_offsets + b + 1) - off;
-    const int64_t len = __ldg(A.cache_len + b);
+    if (*last < 0) return;
+    if (mine.b == *last) *slot = mine;
+    __syncthreads();
+    const int b = slot->b;
+    const int64_t off = slot->off, n = slot->n, len = slot->len;
     if (n == 0) return;
     if (len < 0) {
         if (threadIdx.x == 0) flag(ERRF_COUNT);
         return;
     }
     const int64_t pi = len / A.page + (pj - (off / A.page + 2 * (int64_t)b));
-    const int64_t first = max(len, pi * A.page), last = min(len + n, (pi + 1) * A.page);
-    if (first >= last) return;
+    const int64_t first = max(len, pi * A.page), end = min(len + n, (pi + 1) * A.page);
+    if (first >= end) return;
     const int32_t page = page_of(A.page_table, A.max_pages, A.n_pages, b, pi);
     if (page < 0) return;
     const void *src = tensor ? A.v : A.k;
@@ -267,13 +327,13 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, in
     uint8_t *cache = (uint8_t *)(tensor ? A.v_cache : A.k_cache) + ((int64_t)page * A.H + h) * A.page * A.D;
     float *scale = (tensor ? A.v_scale : A.k_scale) + (int64_t)page * A.H + h;
     const int held = (int)(first - pi * A.page);  // tokens that the page holds already
-    const int upr = A.D / 16, units = (int)(last - first) * upr;
+    const int upr = A.D / 16, units = (int)(end - first) * upr;
 
-    float x[APPEND_PAGE_UNITS][16];
+    float x[U][16];
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < APPEND_PAGE_UNITS; k++) {
-        const int i = threadIdx.x + k * APPEND_PAGE_THREADS;
+    for (int k = 0; k < U; k++) {
+        const int i = threadIdx.x + k * APPEND_THREADS;
         if (i < units) {
             const int64_t pos = first + i / upr;
             const int u = i % upr;
@@ -286,10 +346,16 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, in
             load_run8<DT>(src, se + ra, xa);
             load_run8<DT>(src, se + rb, xb);
             if (rot) {
-                float c[8], s[8];
 #pragma unroll
-                for (int t = 0; t < 8; t++) turn(pos, __ldg(A.inv_freq + u * 8 + t), c[t], s[t]);
-                rotate_unit(A.interleaved, c, s, xa, xb);
+                for (int t = 0; t < 8; t++) {  // (a pair at a time: cos and sin of eight would cost 16 registers)
+                    float c, s;
+                    turn(pos, __ldg(A.inv_freq + u * 8 + t), c, s);
+                    float &x1 = !A.interleaved ? xa[t] : (t < 4 ? xa[2 * t] : xb[2 * (t - 4)]);
+                    float &x2 = !A.interleaved ? xb[t] : (t < 4 ? xa[2 * t + 1] : xb[2 * (t - 4) + 1]);
+                    const float y1 = x1 * c - x2 * s;
+                    x2 = x2 * c + x1 * s;
+                    x1 = y1;
+                }
             }
 #pragma unroll
             for (int t = 0; t < 8; t++) {
@@ -308,7 +374,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, in
     const float before = held ? *scale : 0.f;
     __syncthreads();  // (also: every thread has read the old scale)
 #pragma unroll
-    for (int wi = 0; wi < APPEND_PAGE_THREADS / 32; wi++) amax = fmaxf(amax, red[wi]);
+    for (int wi = 0; wi < APPEND_THREADS / 32; wi++) amax = fmaxf(amax, red[wi]);
     float now = e4m3_scale(amax);
     if (held) {
         if (!(before >= 0.f) || before > 3.4028235e38f) {
@@ -317,7 +383,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, in
             now = before;
         } else {
             const float f = before / now;
-            for (int i = threadIdx.x; i < held * upr; i += APPEND_PAGE_THREADS) {
+            for (int i = threadIdx.x; i < held * upr; i += APPEND_THREADS) {
                 uint4 w = *(uint4 *)(cache + (int64_t)i * 16);
                 uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -329,32 +395,44 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, in
         }
     }
     if (threadIdx.x == 0) *scale = now;
+    const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+    const float inv = 1.f / now;
 #pragma unroll
-    for (int k = 0; k < APPEND_PAGE_UNITS; k++) {
-        const int i = threadIdx.x + k * APPEND_PAGE_THREADS;
+    for (int k = 0; k < U; k++) {
+        const int i = threadIdx.x + k * APPEND_THREADS;
         if (i < units) {
             const int u = i % upr;
             int ra, rb;
             if (!tensor && u < A.rot / 16) unit_runs(A, u, ra, rb);
             else { ra = u * 16; rb = ra + 8; }
             uint8_t *row = cache + (int64_t)(held + i / upr) * A.D;
-            // (a quotient, not a product with 1 / now: a scale kept from the page's own history need not be a power of two)
-            *(uint2 *)(row + ra) = make_uint2(pack_e4m3x4(x[k][0] / now, x[k][1] / now, x[k][2] / now, x[k][3] / now),
-                                              pack_e4m3x4(x[k][4] / now, x[k][5] / now, x[k][6] / now, x[k][7] / now));
-            *(uint2 *)(row + rb) = make_uint2(pack_e4m3x4(x[k][8] / now, x[k][9] / now, x[k][10] / now, x[k][11] / now),
-                                              pack_e4m3x4(x[k][12] / now, x[k][13] / now, x[k][14] / now, x[k][15] / now));
+            // (the reciprocal of a power of two is exact; a scale that the page had need not be one)
+            if (!pow2) {
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[k][e] /= now;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[k][e] *= inv;
+            }
+            *(uint2 *)(row + ra) = make_uint2(pack_e4m3x4(x[k][0], x[k][1], x[k][2], x[k][3]), pack_e4m3x4(x[k][4], x[k][5], x[k][6], x[k][7]));
+            *(uint2 *)(row + rb) = make_uint2(pack_e4m3x4(x[k][8], x[k][9], x[k][10], x[k][11]), pack_e4m3x4(x[k][12], x[k][13], x[k][14], x[k][15]));
         }
     }
 }
 
-template <int DT, bool FP8>
-__global__ void __launch_bounds__(APPEND_PAGE_THREADS) k_kv_append(const AppendArgs A)
+// U: units a thread of a page's CTA (0: no E4M3 cache).  A CTA's chain of reads is long against its work, so the CTAs
+// that an SM holds count for more than a few spilled registers: five of them (48 registers) took 74 us where three (77)
+// took 86 (8 chunks into an E4M3 cache), 143 where four took 158 (16384 tokens into a bf16 one).
+template <int DT, int U>
+__global__ void __launch_bounds__(APPEND_THREADS, U <= 2 ? 5 : 2) k_kv_append(const AppendArgs A)
 {
-    extern __shared__ float2 cs[];  // [rot / 2] cos, sin of the token
-    __shared__ int slot;
-    __shared__ float red[APPEND_PAGE_THREADS / 32];
-    if (!FP8 || (int64_t)blockIdx.x < A.row_ctas) append_rows<DT, !FP8>(A, cs, &slot);
-    else if constexpr (FP8) append_page<DT>(A, (int64_t)blockIdx.x - A.row_ctas, &slot, red);
+    extern __shared__ float2 cs[];  // [tokens][rot / 2] cos, sin
+    __shared__ SeqOf slots[APPEND_TOKENS];
+    __shared__ int32_t pages[APPEND_TOKENS];
+    __shared__ int last;
+    __shared__ float red[APPEND_THREADS / 32];
+    if (U == 0 || (int64_t)blockIdx.x < A.row_ctas) append_rows<DT, U == 0>(A, cs, slots, pages);
+    else if constexpr (U > 0) append_page<DT, U>(A, (int64_t)blockIdx.x - A.row_ctas, slots, &last, red);
 }
 
 }  // namespace lsa

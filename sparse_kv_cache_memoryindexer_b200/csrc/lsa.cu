@@ -1097,20 +1097,25 @@ lsa_status check_rows(const char *what, const char *name, const void *p, int64_t
     return LSA_OK;
 }
 
-template <int DT, bool FP8>
+template <int DT, int U>
 lsa_status launch_append(AppendArgs &A, cudaStream_t st)
 {
+    constexpr bool FP8 = U > 0;
     const int64_t rows = (A.q ? A.Hq : 0) + (FP8 ? 0 : 2 * A.H);
     const int64_t units = rows * (A.D / 16);
-    // few tokens: a token's rows are spread over CTAs until there are about four for each SM
-    const int64_t want = (4 * (int64_t)num_sms() + A.N - 1) / A.N, most = (units + APPEND_PAGE_THREADS - 1) / APPEND_PAGE_THREADS;
+    // few tokens: a token's rows are spread over CTAs until there are about four for each SM; many: a CTA takes several,
+    // for about eight units a thread, while there are still about eight CTAs for each SM
+    const int64_t sms = num_sms(), want = (4 * sms + A.N - 1) / A.N, most = (units + APPEND_THREADS - 1) / APPEND_THREADS;
     A.row_ctas_per_token = (int)(want < most ? want : most);
-    A.row_ctas = A.N * A.row_ctas_per_token;
+    const int64_t several = units > 0 ? std::min<int64_t>((8 * APPEND_THREADS + units - 1) / units, A.N / (8 * sms)) : 1;
+    A.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(several, APPEND_TOKENS));
+    if (A.tokens > 1) A.row_ctas_per_token = 1;
+    A.row_ctas = (A.N + A.tokens - 1) / A.tokens * A.row_ctas_per_token;
     const int64_t jobs = FP8 ? (A.N / A.page + 2 * (int64_t)A.B) * A.H * 2 : 0;
     const int64_t grid = A.row_ctas + jobs;
     LSA_REQUIRE(grid < (int64_t)1 << 31, "lsa_kv_append: too many rows for one launch");
     if (grid == 0) return LSA_OK;
-    k_kv_append<DT, FP8><<<(unsigned)grid, APPEND_PAGE_THREADS, sizeof(float2) * (size_t)(A.rot / 2), st>>>(A);
+    k_kv_append<DT, U><<<(unsigned)grid, APPEND_THREADS, sizeof(float2) * (size_t)(A.rot / 2) * A.tokens, st>>>(A);
     return launched("append to the window cache");
 }
 
@@ -1188,9 +1193,12 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
     A.N = N; A.n_pages = n_pages; A.B = B; A.max_pages = max_pages; A.Hq = H_q; A.H = H_kv; A.D = D;
     A.page = page_size; A.rot = rot_dim; A.interleaved = interleaved != 0;
     cudaStream_t st = (cudaStream_t)stream;
-    if (dt == LSA_F32) LSA_TRY((launch_append<DT_F32, false>(A, st)));
-    else if (cdt == LSA_BF16) LSA_TRY((launch_append<DT_BF16, false>(A, st)));
-    else LSA_TRY((launch_append<DT_BF16, true>(A, st)));
+    const int units = page_size * D / 16;  // of a page and head
+    if (dt == LSA_F32) LSA_TRY((launch_append<DT_F32, 0>(A, st)));
+    else if (cdt == LSA_BF16) LSA_TRY((launch_append<DT_BF16, 0>(A, st)));
+    else if (units <= APPEND_THREADS) LSA_TRY((launch_append<DT_BF16, 1>(A, st)));
+    else if (units <= 2 * APPEND_THREADS) LSA_TRY((launch_append<DT_BF16, 2>(A, st)));
+    else LSA_TRY((launch_append<DT_BF16, 4>(A, st)));
     return ok();
 }
 
