@@ -1244,7 +1244,7 @@ lsa_status lsa_core_attention(const void *q, int64_t q_stride, lsa_dtype dt, con
     LSA_REQUIRE(k >= 1 && k <= LSA_MAX_TOPK, "%s: k must be in [1, %d]", what, LSA_MAX_TOPK);
     LSA_REQUIRE(total_S >= 0 && total_S < (int64_t)1 << 31, "%s: total_S must be in [0, 2^31)", what);
     LSA_REQUIRE(W >= 0 && (W == 0) == (win_kv == nullptr), "%s: win_kv is given exactly when W > 0", what);
-    LSA_REQUIRE((int64_t)B * W < (int64_t)1 << 31 && B > 0, "%s: B * W must be below 2^31", what);
+    LSA_REQUIRE((int64_t)B * W < (int64_t)1 << 31, "%s: B * W must be below 2^31", what);
     LSA_REQUIRE(dt == LSA_F32 || dt == LSA_BF16, "%s: dt must be F32 or BF16", what);
     LSA_REQUIRE(H_kv > 0 && D > 0 && row_bytes == 2 * (size_t)H_kv * D * elem_bytes(dt),
                 "%s: row_bytes must be 2 * H_kv * D elements", what);

@@ -516,10 +516,6 @@ def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_sc
                   interleaved=False, q=None, q_out=None, stream=None):
     """Rotate the new tokens' keys (and queries) to their positions and write keys and values into the
     paged window cache (see include/lsa.h).  q, k, v [N][heads][D] may be slices of one fused projection."""
-    dev = _placed("lsa_kv_append",
-                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("inv_freq", inv_freq),
-                   ("q_out", q_out)), (("k", k), ("v", v), ("q", q)))
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_kv_append", q_offsets, cache_len, page_table, k_cache, v_cache,
                                                       k_scale, v_scale)
     dt = k.dtype
@@ -546,6 +542,10 @@ def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_sc
         if inv_freq.dtype != torch.float32:
             _need(torch.float32, inv_freq=inv_freq)
         rot = 2 * inv_freq.numel()
+    dev = _placed("lsa_kv_append",
+                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
+                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("inv_freq", inv_freq),
+                   ("q_out", q_out)), (("k", k), ("v", v), ("q", q)))
     _on(dev, stream, _lib.lsa_kv_append, _ptr(q), sq, k.data_ptr(), sk, v.data_ptr(), sv, DTYPE_CODE[dt],
         q_offsets.data_ptr(), N, B, cache_len.data_ptr(), page_table.data_ptr(), max_pages, _ptr(inv_freq), rot,
         1 if interleaved else 0, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode, _ptr(k_scale),
@@ -577,13 +577,13 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
                          softmax_scale=None, k_scale=None, v_scale=None, lse_out=None, stream=None):
     """Attention over the paged window cache: a sliding window of `window` tokens (0: no limit) and the
     first n_sink tokens (see include/lsa.h).  softmax_scale defaults to D ** -0.5."""
+    B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
+                                                      v_cache, k_scale, v_scale)
+    code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
     dev = _placed("lsa_window_attention",
                   (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
                    ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("out", out), ("lse_out", lse_out),
                    ("workspace", workspace)), (("q", q),))
-    B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
-                                                      v_cache, k_scale, v_scale)
-    code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
     _on(dev, stream, _lib.lsa_window_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode,
         _ptr(k_scale), _ptr(v_scale), window, n_sink, D ** -0.5 if softmax_scale is None else softmax_scale,
@@ -599,11 +599,6 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
                        stream=None):
     """One softmax over each query's Top-k entries (rows of hot_kv, or of win_kv for entries compressed
     during the window) and its window of the paged cache (see include/lsa.h)."""
-    dev = _placed("lsa_core_attention",
-                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("topk_idx", topk_idx), ("idx", idx), ("count", count),
-                   ("seq_offsets", seq_offsets), ("hot_kv", hot_kv), ("win_kv", win_kv), ("out", out),
-                   ("lse_out", lse_out), ("workspace", workspace)), (("q", q),))
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_core_attention", q_offsets, cache_len, page_table, k_cache,
                                                       v_cache, None, None)
     code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
@@ -630,6 +625,11 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
             win_kv = None
         elif win_kv.numel() * win_kv.element_size() < B * W * row_bytes:
             _cap_bytes(B * W * row_bytes, win_kv=win_kv)
+    dev = _placed("lsa_core_attention",
+                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
+                   ("v_cache", v_cache), ("topk_idx", topk_idx), ("idx", idx), ("count", count),
+                   ("seq_offsets", seq_offsets), ("hot_kv", hot_kv), ("win_kv", win_kv), ("out", out),
+                   ("lse_out", lse_out), ("workspace", workspace)), (("q", q),))
     _on(dev, stream, _lib.lsa_core_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), window, n_sink,
         D ** -0.5 if softmax_scale is None else softmax_scale, topk_idx.data_ptr(), k, idx.data_ptr(), count.data_ptr(),

@@ -1,8 +1,10 @@
-"""One trigger window of the LSA indexer path on one GPU: buffers plus the five C-ABI calls.
+"""One trigger window of the LSA indexer path on one GPU: buffers plus the five C-ABI calls, and the
+decode steps inside it.
 
 Allocation and call order only (PyTorch holds the device memory); every stage is a kernel
 of liblsa.so.  Order of the stages follows the hyper.ai summary ("Method") and the blog
-review's sections 3-3.2: project -> score/threshold/OR/compact -> fetch -> Lightning Top-k.
+review's sections 3-3.2: project -> score/threshold/OR/compact -> fetch -> Lightning Top-k; at each
+decode step Top-k -> append to the window cache -> core attention over both.
 """
 from __future__ import annotations
 
@@ -21,6 +23,45 @@ def _stage(name):
         yield
     finally:
         torch.cuda.nvtx.range_pop()
+
+
+class WindowCache:
+    """The keys and values that stay on the GPU, in pages: the sliding window and the first tokens (the rest
+    of the context is reached through the fetched entries).  Which pages a sequence has is the caller's:
+    page_table [B][max_pages] holds a page number for every page_size tokens that some query can still see
+    or that a new token falls on, and -1 elsewhere (a page behind the window may be given to others).
+
+    cdtype float8_e4m3fn keeps the cache in 8 bits with one scale per page and head."""
+
+    def __init__(self, B, H_kv, D, page_size, n_pages, max_pages, dtype, cdtype=None, window=0, n_sink=0, device="cuda"):
+        dev = torch.device(device)
+        self.B, self.H_kv, self.D, self.page_size = B, H_kv, D, page_size
+        self.dtype, self.cdtype, self.window, self.n_sink = dtype, dtype if cdtype is None else cdtype, window, n_sink
+        shape = (n_pages, H_kv, page_size, D)
+        self.k = torch.empty(shape, dtype=self.cdtype, device=dev)
+        self.v = torch.empty(shape, dtype=self.cdtype, device=dev)
+        fp8 = self.cdtype == torch.float8_e4m3fn
+        self.k_scale = torch.empty((n_pages, H_kv), dtype=torch.float32, device=dev) if fp8 else None
+        self.v_scale = torch.empty((n_pages, H_kv), dtype=torch.float32, device=dev) if fp8 else None
+        self.page_table = torch.full((B, max_pages), -1, dtype=torch.int32, device=dev)
+        self.len = torch.zeros(B, dtype=torch.int32, device=dev)  # tokens of each sequence so far
+
+    def append(self, k, v, q_offsets, inv_freq=None, interleaved=False, q=None, q_out=None, stream=None):
+        """Writes the new tokens' keys and values (rotated to their positions); `len` still counts the
+        tokens before them, which is what attend() of the same tokens wants; advance() moves it on."""
+        lsa.lsa_kv_append(k, v, q_offsets, self.len, self.page_table, self.k, self.v, k_scale=self.k_scale,
+                          v_scale=self.v_scale, inv_freq=inv_freq, interleaved=interleaved, q=q, q_out=q_out,
+                          stream=stream)
+
+    def attend(self, q, q_offsets, out, workspace, softmax_scale=None, lse_out=None, stream=None):
+        """Attention of the tokens last appended over the window and the first tokens."""
+        lsa.lsa_window_attention(q, q_offsets, self.len, self.page_table, self.k, self.v, out, workspace,
+                                 window=self.window, n_sink=self.n_sink, softmax_scale=softmax_scale,
+                                 k_scale=self.k_scale, v_scale=self.v_scale, lse_out=lse_out, stream=stream)
+
+    def advance(self, q_offsets):
+        """Counts the appended tokens (on the current stream)."""
+        self.len += (q_offsets[1:] - q_offsets[:-1]).to(torch.int32)
 
 
 class IndexerPath:
@@ -139,3 +180,47 @@ class IndexerPath:
         rec(ev[4], st)
         st.wait_event(rows_done)
         rec(ev[6], st)
+
+    def open_decode(self, cache, H_q, W=0):
+        """Buffers for decode_step: one token per sequence, H_q query heads over `cache` (whose rows and the
+        fetched rows must agree: row_bytes = 2 * H_kv * D elements), up to W entries compressed in the window."""
+        dev = self.idx.device
+        esize = torch.empty((), dtype=cache.dtype).element_size()
+        if self.row_bytes != 2 * cache.H_kv * cache.D * esize or cache.cdtype != cache.dtype:
+            raise ValueError(f"the fetched rows ({self.row_bytes} bytes) must be [2][H_kv][D] of the cache's type")
+        if cache.B != self.B:
+            raise ValueError(f"the cache holds {cache.B} sequences, the path {self.B}")
+        self.cache, self.H_q, self.W = cache, H_q, W
+        u8 = torch.uint8
+        self.step_idx = torch.empty((self.B, self.k), dtype=torch.int32, device=dev)
+        self.step_score = torch.empty((self.B, self.k), dtype=torch.float32, device=dev)
+        self.ws_step = torch.empty(max(lsa.lsa_lightning_topk_step_workspace_size(self.B, self.total_S, self.n_h, self.d_I, W), 256),
+                                   dtype=u8, device=dev)
+        self.ws_core = torch.empty(lsa.lsa_core_attention_workspace_size(self.B, self.B, H_q, cache.H_kv, cache.D, self.k),
+                                   dtype=u8, device=dev)
+        self.q_rot = torch.empty((self.B, H_q, cache.D), dtype=cache.dtype, device=dev)
+        self.attn_out = torch.empty((self.B, H_q, cache.D), dtype=cache.dtype, device=dev)
+        self.attn_lse = torch.empty((self.B, H_q), dtype=torch.float32, device=dev)
+        self.one_each = torch.arange(self.B + 1, dtype=torch.int64, device=dev)
+
+    def decode_step(self, q_step, w_step, q, k, v, seq_offsets, win_K=None, win_scale=None, win_count=None, win_kv=None,
+                    inv_freq=None, interleaved=False, softmax_scale=None, stream=None):
+        """One decode step of every sequence: the Lightning Top-k of its indexer query over the fetched entries
+        (and the win_count entries compressed since the trigger: keys win_K, rows win_kv), the new token's q, k, v
+        [B][heads][D] rotated and k, v appended to the window cache, and one softmax over the Top-k rows, the
+        window and the first tokens.  Returns attn_out [B][H_q][D] (step_idx, attn_lse beside it); cache.advance
+        follows once every layer is done.  Launches only kernels: a step can be recorded in a CUDA graph."""
+        c = self.cache
+        with _stage("lsa.lightning_topk_step"):
+            lsa.lsa_lightning_topk_step(q_step, w_step, self.hot_K, self.hot_scale, self.idx, self.count, seq_offsets,
+                                        self.total_S, self.k, self.step_idx, self.ws_step, win_K=win_K,
+                                        win_scale=win_scale, win_count=win_count, topk_score=self.step_score,
+                                        stream=stream)
+        with _stage("lsa.kv_append"):
+            c.append(k, v, self.one_each, inv_freq=inv_freq, interleaved=interleaved, q=q, q_out=self.q_rot, stream=stream)
+        with _stage("lsa.core_attention"):
+            lsa.lsa_core_attention(self.q_rot, self.one_each, c.len, c.page_table, c.k, c.v, self.step_idx, self.idx,
+                                   self.count, seq_offsets, self.total_S, self.hot_kv, self.attn_out, self.ws_core,
+                                   win_kv=win_kv, window=c.window, n_sink=c.n_sink, softmax_scale=softmax_scale,
+                                   lse_out=self.attn_lse, stream=stream)
+        return self.attn_out

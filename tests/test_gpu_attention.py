@@ -454,3 +454,62 @@ def test_pages_past_32_bits(m):
         assert torch.equal(d["out"], want["out"])
         del d
         torch.cuda.empty_cache()
+
+
+def test_core_attention_long_fetch_lists(m):
+    """Fetch lists longer than the shared memory that they are searched in: every 2^i-th entry of them."""
+    for dt, D, fetched in ((BF16, 32, [15000, 6140, 6145]), (BF16, 64, [30000, 1, 0])):
+        c = Case([1, 1, 1], [20, 500, 0], 2, 4, D, 16, dt, window=40, sinks=2)
+        c.add_topk(100, [40000, 9000, 7000], fetched, 3)
+        run(m, c)
+
+
+def test_core_attention_of_many_users_and_full_lists(m):
+    """Shared out over the CTAs instead of clusters (long lists, a long window), and 4096 entries a token."""
+    c = Case([1] * 5, [9000, 0, 40, 5000, 100], 2, 16, 64, 64, BF16, window=5000, sinks=1)
+    run(m, c.add_topk(4096, [6000] * 5, [5000, 4095, 10, 4100, 0], 4))
+
+
+def test_many_sequences(m):
+    """More sequences than a CTA has threads, empty ones among them, in both ways of sharing the work."""
+    new = [(i * 7) % 3 for i in range(300)]
+    old = [(i * 37) % 200 for i in range(300)]
+    rows = {(b, i) for b in range(0, 300, 23) for i in range(new[b])} | {(299, i) for i in range(new[299])}
+    for cdt, window in ((BF16, 0), (BF16, 60), (ao.E4M3, 0), (F32, 50)):
+        run(m, Case(new, old, 1, 4, 64, 16, F32 if cdt == F32 else BF16, cdt, window=window), rows)
+    old[17] = 20000
+    run(m, Case(new, old, 1, 4, 64, 128, BF16, BF16), rows | {(17, i) for i in range(new[17])})
+
+
+def test_negative_and_zero_scale(m):
+    """softmax_scale may have any sign; zero weighs every visible key alike."""
+    for n in (1, 50):
+        for cdt in (BF16, ao.E4M3, F32):
+            for scale in (-0.3, 0.0):
+                c = Case([n, n], [100, 7], 2, 8, 64, 32, F32 if cdt == F32 else BF16, cdt, window=60, sinks=2)
+                c.scale = scale
+                d = c.cuda()
+                call(m, c, d, softmax_scale=scale)
+                m.lsa_check_device()
+                out, lse = d["out"].cpu().double(), d["lse_out"].cpu().double()
+                assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+                check_signed(c, out, lse)
+
+
+def check_signed(case, out, lse):
+    G = case.Hq // case.H
+    p_dtype = {BF16: BF16, F32: None, ao.E4M3: torch.float16}[case.cdt]
+    for b, (n, old) in enumerate(zip(case.new, case.old)):
+        for i in {0, n // 2, n - 1}:
+            j = torch.tensor(ao.visible(old + i, old + n, case.window, case.sinks))
+            pg, sl = case.table[b].long()[j // case.page], j % case.page
+            at = int(case.offs[b]) + i
+            for hq in range(case.Hq):
+                h = hq // G
+                K, V = case.kc[pg, :, sl][:, h].double(), case.vc[pg, :, sl][:, h].double()
+                if case.ks is not None:
+                    K, V = K * case.ks[pg, h].double()[:, None], V * case.vs[pg, h].double()[:, None]
+                o, l_, A, mag = ao.attend(case.q[at, hq].double(), K, V, case.scale)
+                bo, bl = ao.attend_bounds(o, A, abs(mag), K.shape[0], case.D, case.dt, p_dtype)
+                assert ((out[at, hq] - o).abs() <= bo).all(), (b, i, hq)
+                assert abs(float(lse[at, hq]) - l_) <= bl, (b, i, hq)
