@@ -303,16 +303,22 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    // the query rows, D / 8 lanes a row, into the swizzled tiles
+    // the query rows, D / 8 lanes a row, into the swizzled tiles; their addresses first, a row a thread (in the space of
+    // the first key tile)
+    int64_t *row_at = (int64_t *)(base + C::OFF_K);
+    for (int r = tid; r < CTA_ROWS; r += C::THREADS) {
+        int64_t n, pos;
+        int g;
+        row_of(A, j, min(r, j.rows - 1), n, pos, g);
+        row_at[r] = r < j.rows ? n * A.q_stride + (int64_t)(h * G + g) * D : -1;
+    }
+    __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < CTA_ROWS * (D / 8); i += C::THREADS) {
         const int r = i / (D / 8), c = i % (D / 8);
+        const int64_t from = row_at[r];
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < j.rows) {
-            int64_t n, pos;
-            int g;
-            row_of(A, j, r, n, pos, g);
-            v = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + n * A.q_stride + (int64_t)(h * G + g) * D) + c);
-        }
+        if (from >= 0) v = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + from) + c);
         if (A.scale < 0.f) {  // the scores' factor is |scale|: the sign goes to the query
             v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
         }
@@ -525,21 +531,34 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         int issued = 0;
         int specials = 0;
         bool special = false;
+        // Page numbers are read two blocks ahead, an E4M3 page's scales one: with the reads in the loop's way a block of
+        // an E4M3 history took 6600 clocks.
+        auto read_page = [&](int i) -> int32_t {  // (-1: no query sees it, or there is no such block)
+            if (i >= nb) return -1;
+            const int64_t pa = block_pos(i0 + i) + (int64_t)lane * A.page;
+            if (lane >= per_block || pa > j.last || (pa + A.page <= j.low && pa >= A.n_sink)) return -1;
+            const int32_t p = __ldg(A.page_table + (int64_t)j.b * A.max_pages + pa / A.page);
+            return p < 0 ? -2 : p;  // (-2: seen, and not there)
+        };
+        auto good_page = [&](int32_t p) { return p >= 0 && p < A.n_pages; };
+        auto read_scale = [&](const float *s, int32_t p) { return FP8 && good_page(p) ? __ldg(s + (int64_t)p * A.H + h) : 1.f; };
+        int32_t page1 = read_page(0), page2 = read_page(1);
+        float ks1 = read_scale(A.k_scale, page1), vs1 = read_scale(A.v_scale, page1);
         for (int i = 0; i < nb; i++) {
-            const int64_t p0 = block_pos(i0 + i), pa = p0 + (int64_t)lane * A.page;
-            const bool see = lane < per_block && pa <= j.last && (pa + A.page > j.low || pa < A.n_sink);
-            int32_t page = -1;
-            float ks = 1.f, vs = 1.f;
-            if (see) {
-                page = page_of(A.page_table, A.max_pages, A.n_pages, j.b, pa / A.page);
-                if (FP8 && page >= 0) {
-                    ks = __ldg(A.k_scale + (int64_t)page * A.H + h);
-                    vs = __ldg(A.v_scale + (int64_t)page * A.H + h);
-                    if (!good_scale(ks) || !good_scale(vs)) {
-                        flag(ERRF_SCALE);
-                        page = -1;
-                    }
-                }
+            const int64_t p0 = block_pos(i0 + i);
+            int32_t page = page1;
+            const float ks = ks1, vs = vs1;
+            page1 = page2;
+            page2 = read_page(i + 2);
+            ks1 = read_scale(A.k_scale, page1);
+            vs1 = read_scale(A.v_scale, page1);
+            if (page != -1 && !good_page(page)) {
+                flag(ERRF_PAGE);
+                page = -1;
+            }
+            if (FP8 && page >= 0 && (!good_scale(ks) || !good_scale(vs))) {
+                flag(ERRF_SCALE);
+                page = -1;
             }
             const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
             const uint32_t bytes = (uint32_t)__popc(there) * page_bytes * boxes;
@@ -590,16 +609,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 int gap0, gap1, end;
                 seen_rows(A, j, p0, gap0, gap1, end);
                 auto seen = [&](int row) { return row < end && (row < gap0 || row >= gap1); };
-                auto loaded = [&](int row) { return (there >> (row / A.page) & 1) != 0; };
-                auto clear = [&](bool of_loaded) {
-                    for (int e = lane; e < BLOCK * 8; e += 32) {
-                        const int row = e >> 3;
-                        if (loaded(row) != of_loaded || (of_loaded && seen(row))) continue;
+                auto clear = [&](int from, int to) {
+                    for (int e = 8 * from + lane; e < 8 * to; e += 32)
 #pragma unroll
                         for (int bx = 0; bx < NB; bx++) *(uint4 *)(vt + bx * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_async();
-                    __syncwarp();
                 };
                 const uint32_t real = vf;
                 const bool part_seen = lane < per_block && page >= 0 &&
@@ -607,7 +620,12 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                                          (gap0 >= gap1 || gap1 <= lane * A.page || gap0 >= lane * A.page + A.page));
                 special = __any_sync(0xffffffffu, part_seen);
                 if (special) vf = landed;
-                if (live != 0xFFu) clear(false);
+                if (live != 0xFFu) {
+                    for (int q = 0; q < per_block; q++)
+                        if (!(there >> q & 1)) clear(q * A.page, (q + 1) * A.page);
+                    fence_async();
+                    __syncwarp();
+                }
                 if (lane == 0) mbar_expect_tx(vf, bytes);
                 __syncwarp();
                 if (page >= 0)
@@ -615,7 +633,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 __syncwarp();
                 if (special) {  // (a few blocks of a CTA's: at the ends of the first tokens, the window, the cache)
                     if (!wait_warp(landed, specials & 1, abort_flag)) break;
-                    clear(true);
+                    clear(gap0, gap1);
+                    clear(end, BLOCK);
+                    fence_async();
+                    __syncwarp();
                     if (lane == 0) mbar_arrive(real);
                     __syncwarp();
                     special = false;
@@ -803,21 +824,37 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
 
 inline int64_t tiles_of(int64_t N, int B, int G) { return N * G / CTA_ROWS + B; }
 
-// CTAs that share one tile's keys: as many as bring the launch to about two for each SM, while the tiles alone do
-// not fill the SMs.
-inline int splits_of(int64_t N, int B, int Hq, int H, int sms)
+// The most CTAs that may share one tile's keys: what brings the launch to about two for each SM.
+inline int most_splits(int64_t N, int Hq, int H, int sms)
 {
-    const int64_t ctas = (N * (Hq / H) / CTA_ROWS > 0 ? N * (Hq / H) / CTA_ROWS : 1) * H;
+    const int64_t ctas = std::max<int64_t>(N * (Hq / H) / CTA_ROWS, 1) * H;
     if (ctas >= sms) return 1;
-    const int64_t z = 2 * (int64_t)sms / ctas;
-    return (int)(z < 1 ? 1 : (z > 16 ? 16 : z));
+    return (int)std::min<int64_t>(16, std::max<int64_t>(1, 2 * (int64_t)sms / ctas));
+}
+
+// CTAs that share one tile's keys, tiles of `blocks` blocks at most: the number with the least time, counted in blocks:
+// the waves of CTAs, each its share of the blocks and about four for its start and end, and about eight for the second
+// launch.  (128 tiles of 34 blocks: 100 us whole, 140 in two parts, which make two waves.)
+inline int splits_of(int64_t N, int Hq, int H, int sms, int64_t blocks)
+{
+    const int64_t ctas = std::max<int64_t>(N * (Hq / H) / CTA_ROWS, 1) * H;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int z = 1; z <= most_splits(N, Hq, H, sms); z++) {
+        const int64_t t = (ctas * z + sms - 1) / sms * ((blocks + z - 1) / z + 4) + (z > 1 ? 8 : 0);
+        if (t < least) {
+            least = t;
+            best = z;
+        }
+    }
+    return best;
 }
 
 inline size_t parts_bytes(int64_t N, int B, int Hq, int H, int D)
 {
     if (Hq % H) return 0;
     int z = 1;  // the most that any number of SMs up to 160 asks for
-    for (int sms = 1; sms <= 160; sms++) z = std::max(z, splits_of(N, B, Hq, H, sms));
+    for (int sms = 1; sms <= 160; sms++) z = std::max(z, most_splits(N, Hq, H, sms));
     if (z == 1) return 0;
     return (size_t)tiles_of(N, B, Hq / H) * H * z * (2 * CTA_ROWS + (size_t)CTA_ROWS * D) * sizeof(float);
 }
@@ -857,7 +894,8 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t tiles = tiles_of(A.N, A.B, A.Hq / A.H);
-    const int Z = splits_of(A.N, A.B, A.Hq, A.H, sms);
+    const int64_t limit = (int64_t)A.max_pages * A.page, seen = A.window > 0 ? std::min(limit, A.window + A.N / A.B) : limit;
+    const int Z = splits_of(A.N, A.Hq, A.H, sms, seen / BLOCK + 1);
     k_attn_many<CT, D><<<dim3((unsigned)tiles, (unsigned)A.H, (unsigned)Z), C::THREADS, C::SMEM, st>>>(A, km, vm, (float *)workspace);
     ++*launches;
     if (Z == 1) return cudaSuccess;
