@@ -313,35 +313,47 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         row_at[r] = r < j.rows ? n * A.q_stride + (int64_t)(h * G + g) * D : -1;
     }
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < CTA_ROWS * (D / 8); i += C::THREADS) {
+    constexpr int PIECES = CTA_ROWS * (D / 8);
+    auto q_at = [&](int i) {
         const int r = i / (D / 8), c = i % (D / 8);
-        const int64_t from = row_at[r];
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (from >= 0) v = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + from) + c);
-        if (A.scale < 0.f) {  // the scores' factor is |scale|: the sign goes to the query
-            v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
+        return C::OFF_Q + (uint32_t)(r >> 7) * C::TILE_BYTES + (uint32_t)(c >> 3) * 16384u + train_tc::sw128(r & 127, c & 7);
+    };
+    if constexpr (!FP8) {
+        for (int i = tid; i < PIECES; i += C::THREADS) {
+            const int64_t from = row_at[i / (D / 8)];
+            few::cp_async16(sbase + q_at(i), (const __nv_bfloat16 *)A.q + (from < 0 ? 0 : from + (i % (D / 8)) * 8), from < 0 ? 0 : 16);
         }
-        if constexpr (FP8) {
-            // f16 by a power of two of the row's own: its largest element comes to [2^8, 2^9)
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        few::cp_commit();
+        few::cp_wait<0>();
+    } else {
+        // f16 by a power of two of the row's own: its largest element comes to [2^8, 2^9)
+        uint4 v[PIECES / C::THREADS];
+#pragma unroll
+        for (int k = 0; k < PIECES / C::THREADS; k++) {
+            const int i = tid + k * C::THREADS;
+            const int64_t from = row_at[i / (D / 8)];
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (from >= 0) v[k] = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + from) + i % (D / 8));
+        }
+#pragma unroll
+        for (int k = 0; k < PIECES / C::THREADS; k++) {
+            const int i = tid + k * C::THREADS;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             float mx = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; k++)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+            for (int e = 0; e < 4; e++)
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
 #pragma unroll
             for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             int e = 8 - ((int)(__float_as_uint(mx) >> 23) - 127);
             e = e > 120 ? 120 : (e < -120 ? -120 : e);
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            if (c == 0) qfac[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (i % (D / 8) == 0) qfac[i / (D / 8)] = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-            for (int k = 0; k < 4; k++)
-                w[k] = few::pack_f16x2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int x2 = 0; x2 < 4; x2++)
+                w[x2] = few::pack_f16x2(__uint_as_float(w[x2] << 16) * up, __uint_as_float(w[x2] & 0xFFFF0000u) * up);
+            *(uint4 *)(base + q_at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const int t = r >> 7, rr = r & 127;
-        *(uint4 *)(base + C::OFF_Q + (uint32_t)t * C::TILE_BYTES + (uint32_t)(c >> 3) * 16384u + train_tc::sw128(rr, c & 7)) = v;
     }
     fence_async();
     tc_fence_before();
@@ -379,6 +391,12 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             for (int pc = 0; pc < 4; pc++) {
                 tmem_ld32(s_addr + 32 * pc, s[pc]);
                 if (pc & 1) tmem_wait_ld();
+            }
+            if (A.scale < 0.f) {  // the scores' factor is |scale|
+#pragma unroll
+                for (int pc = 0; pc < 4; pc++)
+#pragma unroll
+                    for (int k = 0; k < 32; k++) s[pc][k] = -s[pc][k];
             }
             if constexpr (FP8) {
 #pragma unroll
@@ -727,23 +745,34 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             setmaxnreg_dec<C::REGS_DECODE>();
             const int ct = tid - 384;
             constexpr int PER = D / 16;  // 16-code pieces of a row
+            // a thread has piece c of every STEP-th row: the swizzle of its rows is one, and all its loads go out first
+            constexpr int STEP = 128 / PER;
+            const int c = ct % PER, row0 = ct / PER;
+            // (the lanes of the upper box store their halves in the other order: no two on one bank)
+            const int odd = (c >> 2) & 1;
+            const uint32_t box = (uint32_t)(c >> 2) * 16384u;
+            const uint32_t at_a = box + train_tc::sw128(row0, ((2 * c) & 7) + odd), at_b = box + train_tc::sw128(row0, ((2 * c) & 7) + 1 - odd);
             auto convert = [&](uint32_t raw, uint32_t tile, uint32_t live, int gap0, int gap1, int end) {
-#pragma unroll 4
-                for (int e = ct; e < BLOCK * PER; e += 128) {
-                    const int row = e / PER, c = e % PER;
-                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                    if (row < end && (row < gap0 || row >= gap1) && (live >> (row >> 4) & 1)) {
-                        const uint4 w = *(const uint4 *)(base + raw + (uint32_t)e * 16);
-                        few::e4m3x4_to_f16x2(w.x, lo.x, lo.y);
-                        few::e4m3x4_to_f16x2(w.y, lo.z, lo.w);
-                        few::e4m3x4_to_f16x2(w.z, hi.x, hi.y);
-                        few::e4m3x4_to_f16x2(w.w, hi.z, hi.w);
+                const bool all = live == 0xFFu && end == BLOCK && gap0 >= gap1;
+                uint4 w[PER];
+#pragma unroll
+                for (int k = 0; k < PER; k++) w[k] = *(const uint4 *)(base + raw + (uint32_t)(ct + 128 * k) * 16);
+                if (!all) {
+#pragma unroll
+                    for (int k = 0; k < PER; k++) {
+                        const int row = row0 + STEP * k;
+                        if (!(row < end && (row < gap0 || row >= gap1) && (live >> (row >> 4) & 1))) w[k] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    uint8_t *box = base + tile + (uint32_t)(c >> 2) * 16384u;
-                    // the lanes of the upper box store their halves in the other order: no two on one bank
-                    const int a = (2 * c) & 7, odd = (c >> 2) & 1;
-                    *(uint4 *)(box + train_tc::sw128(row, a + odd)) = odd ? hi : lo;
-                    *(uint4 *)(box + train_tc::sw128(row, a + 1 - odd)) = odd ? lo : hi;
+                }
+#pragma unroll
+                for (int k = 0; k < PER; k++) {
+                    uint4 lo, hi;
+                    few::e4m3x4_to_f16x2(w[k].x, lo.x, lo.y);
+                    few::e4m3x4_to_f16x2(w[k].y, lo.z, lo.w);
+                    few::e4m3x4_to_f16x2(w[k].z, hi.x, hi.y);
+                    few::e4m3x4_to_f16x2(w[k].w, hi.z, hi.w);
+                    *(uint4 *)(base + tile + at_a + (uint32_t)(k * STEP) * 128u) = odd ? hi : lo;
+                    *(uint4 *)(base + tile + at_b + (uint32_t)(k * STEP) * 128u) = odd ? lo : hi;
                 }
             };
             for (int i = 0; i < nb; i++) {
