@@ -11,6 +11,8 @@
 //
 // This file: the arguments, and what the kernels share.
 #pragma once
+#include <atomic>
+
 #include "kv_append.cuh"
 
 namespace lsa {
@@ -36,6 +38,21 @@ struct AttnArgs {
     int64_t total_S, row_bytes;
     int k, W;
 };
+
+// Raises a kernel's limit of dynamic shared memory, once per device (the attribute stays): done holds a bit for each
+// of the first 64 devices.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // The keys a query position sees, in the order [first tokens][window]: key number t is position t for
 // t < sinks, else lo + (t - sinks).

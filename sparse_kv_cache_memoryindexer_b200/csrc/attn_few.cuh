@@ -1118,6 +1118,7 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     const int64_t chunks = seen / KEYS + 2 + (A.window > 0 ? (A.n_sink < limit ? A.n_sink : limit) / KEYS + 1 : 0) + list;
     const int64_t likely = CORE ? tiles : A.B * ((n * G + ROWS - 1) / ROWS > 0 ? (n * G + ROWS - 1) / ROWS : 1);
     const size_t smem = C::SMEM + (CORE ? (size_t)list * KEYS * 4 : 0);
+    constexpr size_t most_smem = C::SMEM + (CORE ? LSA_MAX_TOPK * 4 : 0);
     const int per_sm = std::max(1, std::min(CTAS_PER_SM<CT, D>, (int)(227 * 1024 / (smem + 1024))));
     cudaLaunchAttribute attr[1];
     cudaError_t e;
@@ -1129,7 +1130,8 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
         const int64_t ctas = Z * likely * A.H, slots = (int64_t)per_sm * sms;
         if (chunks <= 64 || ctas <= slots || 4 * ctas >= 3 * ((ctas + slots - 1) / slots) * slots) {
             auto kernel = k_attn_few<QT, CT, D, CORE, false>;
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            static std::atomic<uint64_t> done{0};
+            e = allow_smem(kernel, most_smem, done);
             if (e != cudaSuccess) return e;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(tiles * Z), (unsigned)A.H);
@@ -1147,7 +1149,8 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
         }
     }
     auto kernel = k_attn_few<QT, CT, D, CORE, true>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem(kernel, most_smem, done);
     if (e != cudaSuccess) return e;
     const int grid = std::min(per_sm * sms, SPLIT_CTAS);
     k_attn_few<QT, CT, D, CORE, true><<<grid, 32 * WARPS, smem, st>>>(A, parts);

@@ -221,6 +221,13 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, ok);
 }
 
+// One arrival for a warp whose lanes have all done (and fenced) what it tells of.
+__device__ __forceinline__ void arrive_warp(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
 __device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity)
 {
     volatile int never = 0;
@@ -282,19 +289,19 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
 
     if (tid == 0) {
         for (int s = 0; s < 2; s++) {
-            mbar_init(k_full(s), FP8 ? 128 : 1);
+            mbar_init(k_full(s), FP8 ? 4 : 1);
             mbar_init(k_empty(s), 1);
-            mbar_init(v_full(s), FP8 ? 128 : 1);
+            mbar_init(v_full(s), FP8 ? 4 : 1);
             mbar_init(v_empty(s), 1);
             mbar_init(s_full(s), 1);
-            mbar_init(p_full(s), 128);
-            mbar_init(p_half(s), 128);
+            mbar_init(p_full(s), 4);
+            mbar_init(p_half(s), 4);
             mbar_init(o_done(s), 1);
         }
         mbar_init(bar(14), 1);    // (landed, or kraw_full)
-        mbar_init(kraw_empty, 128);
+        mbar_init(kraw_empty, 4);
         mbar_init(vraw_full, 1);
-        mbar_init(vraw_empty, 128);
+        mbar_init(vraw_empty, 4);
         mbar_init(drained, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -325,6 +332,13 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         }
         few::cp_commit();
         few::cp_wait<0>();
+        if (A.scale < 0.f) {  // the scores' factor is |scale|: the sign goes to the query
+#pragma unroll 1
+            for (int i = tid; i < PIECES; i += C::THREADS) {
+                uint4 *p = (uint4 *)(base + q_at(i));
+                *p = make_uint4(p->x ^ 0x80008000u, p->y ^ 0x80008000u, p->z ^ 0x80008000u, p->w ^ 0x80008000u);
+            }
+        }
     } else {
         // f16 by a power of two of the row's own: its largest element comes to [2^8, 2^9)
         uint4 v[PIECES / C::THREADS];
@@ -347,7 +361,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             int e = 8 - ((int)(__float_as_uint(mx) >> 23) - 127);
             e = e > 120 ? 120 : (e < -120 ? -120 : e);
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), A.scale);  // (the scores' factor is |scale|)
             if (i % (D / 8) == 0) qfac[i / (D / 8)] = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
             for (int x2 = 0; x2 < 4; x2++)
@@ -391,12 +405,6 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             for (int pc = 0; pc < 4; pc++) {
                 tmem_ld32(s_addr + 32 * pc, s[pc]);
                 if (pc & 1) tmem_wait_ld();
-            }
-            if (A.scale < 0.f) {  // the scores' factor is |scale|
-#pragma unroll
-                for (int pc = 0; pc < 4; pc++)
-#pragma unroll
-                    for (int k = 0; k < 32; k++) s[pc][k] = -s[pc][k];
             }
             if constexpr (FP8) {
 #pragma unroll
@@ -474,21 +482,17 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     }
                     if (FP8) l = fmaf(sum.x + sum.y, me->inv[2 * pc + gg], l);
                 }
-                if (FP8 && me->zero) {
-#pragma unroll
-                    for (int k = 0; k < 16; k++) u[k] = (me->zero >> (2 * pc + (k >> 3)) & 1) ? 0u : u[k];
-                }
                 tmem_st16(s_addr + 16 * pc, u);
                 if (pc == 1) {  // the product over the first 64 keys can start
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(p_half(t));
+                    arrive_warp(p_half(t));
                 }
             }
             if (!FP8) l += sum.x + sum.y;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(p_full(t));
+            arrive_warp(p_full(t));
         }
         if (ok && !wait_warp(o_done(t), (nb - 1) & 1, abort_flag)) ok = false;
         if (ok) {
@@ -744,8 +748,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         if constexpr (FP8) {
             setmaxnreg_dec<C::REGS_DECODE>();
             const int ct = tid - 384;
+            // (What a warp runs once a block is unrolled in full here and in the softmax: with more of it the SM's
+            // instruction cache no longer held a block's code, and everything took twice as long.)
             constexpr int PER = D / 16;  // 16-code pieces of a row
-            // a thread has piece c of every STEP-th row: the swizzle of its rows is one, and all its loads go out first
+            // a thread has piece c of every STEP-th row: the swizzle of its rows is one
             constexpr int STEP = 128 / PER;
             const int c = ct % PER, row0 = ct / PER;
             // (the lanes of the upper box store their halves in the other order: no two on one bank)
@@ -754,44 +760,51 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             const uint32_t at_a = box + train_tc::sw128(row0, ((2 * c) & 7) + odd), at_b = box + train_tc::sw128(row0, ((2 * c) & 7) + 1 - odd);
             auto convert = [&](uint32_t raw, uint32_t tile, uint32_t live, int gap0, int gap1, int end) {
                 const bool all = live == 0xFFu && end == BLOCK && gap0 >= gap1;
-                uint4 w[PER];
+#pragma unroll 1
+                for (int k0 = 0; k0 < PER; k0 += 4) {
+                    const uint8_t *from = base + raw + (uint32_t)(ct + 128 * k0) * 16;
+                    uint8_t *to = base + tile + (uint32_t)(k0 * STEP) * 128u;
+                    uint4 w[4];
 #pragma unroll
-                for (int k = 0; k < PER; k++) w[k] = *(const uint4 *)(base + raw + (uint32_t)(ct + 128 * k) * 16);
-                if (!all) {
+                    for (int k = 0; k < 4; k++) w[k] = *(const uint4 *)(from + 2048 * k);
+                    if (!all) {
 #pragma unroll
-                    for (int k = 0; k < PER; k++) {
-                        const int row = row0 + STEP * k;
-                        if (!(row < end && (row < gap0 || row >= gap1) && (live >> (row >> 4) & 1))) w[k] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int k = 0; k < 4; k++) {
+                            const int row = row0 + STEP * (k0 + k);
+                            if (!(row < end && (row < gap0 || row >= gap1) && (live >> (row >> 4) & 1))) w[k] = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < PER; k++) {
-                    uint4 lo, hi;
-                    few::e4m3x4_to_f16x2(w[k].x, lo.x, lo.y);
-                    few::e4m3x4_to_f16x2(w[k].y, lo.z, lo.w);
-                    few::e4m3x4_to_f16x2(w[k].z, hi.x, hi.y);
-                    few::e4m3x4_to_f16x2(w[k].w, hi.z, hi.w);
-                    *(uint4 *)(base + tile + at_a + (uint32_t)(k * STEP) * 128u) = odd ? hi : lo;
-                    *(uint4 *)(base + tile + at_b + (uint32_t)(k * STEP) * 128u) = odd ? lo : hi;
+                    for (int k = 0; k < 4; k++) {
+                        uint4 lo, hi;
+                        few::e4m3x4_to_f16x2(w[k].x, lo.x, lo.y);
+                        few::e4m3x4_to_f16x2(w[k].y, lo.z, lo.w);
+                        few::e4m3x4_to_f16x2(w[k].z, hi.x, hi.y);
+                        few::e4m3x4_to_f16x2(w[k].w, hi.z, hi.w);
+                        *(uint4 *)(to + at_a + (uint32_t)(k * STEP) * 128u) = odd ? hi : lo;
+                        *(uint4 *)(to + at_b + (uint32_t)(k * STEP) * 128u) = odd ? lo : hi;
+                    }
                 }
             };
             for (int i = 0; i < nb; i++) {
                 const int64_t p0 = block_pos(i0 + i);
                 int gap0, gap1, end;
                 seen_rows(A, j, p0, gap0, gap1, end);
-                if (!wait_warp(kraw_full, i & 1, abort_flag)) break;
-                const uint32_t live = meta[i & (META - 1)].live;
-                if (!wait_warp(k_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
-                convert(C::OFF_KRAW, C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES, live, gap0, gap1, end);
-                fence_async();
-                mbar_arrive(k_full(i & 1));
-                mbar_arrive(kraw_empty);
-                if (!wait_warp(vraw_full, i & 1, abort_flag)) break;
-                if (!wait_warp(v_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag)) break;
-                convert(C::OFF_VRAW, C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES, live, gap0, gap1, end);
-                fence_async();
-                mbar_arrive(v_full(i & 1));
-                mbar_arrive(vraw_empty);
+                bool go = true;
+#pragma unroll 1
+                for (int v = 0; v < 2 && go; v++) {  // keys, values (one body for both: see below)
+                    const uint32_t raw_full = v ? vraw_full : kraw_full, empty = v ? v_empty(i & 1) : k_empty(i & 1);
+                    go = wait_warp(raw_full, i & 1, abort_flag) && wait_warp(empty, ((i >> 1) & 1) ^ 1, abort_flag);
+                    if (!go) break;
+                    const Meta &me = meta[i & (META - 1)];
+                    // (values of a page whose scale is zero are zeros: its keys have their share of the sum, no more)
+                    convert(v ? C::OFF_VRAW : C::OFF_KRAW, (v ? C::OFF_V : C::OFF_K) + (uint32_t)(i & 1) * C::TILE_BYTES,
+                            v ? me.live & ~me.zero : me.live, gap0, gap1, end);
+                    fence_async();
+                    arrive_warp(v ? v_full(i & 1) : k_full(i & 1));
+                    arrive_warp(v ? vraw_empty : kraw_empty);
+                }
+                if (!go) break;
             }
         }
     }
@@ -920,7 +933,8 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     if (!make_cache_map(&km, A.k_cache, CT == DT_FP8, rows, D, A.page) || !make_cache_map(&vm, A.v_cache, CT == DT_FP8, rows, D, A.page))
         return cudaErrorInvalidValue;
     auto kernel = k_attn_many<CT, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kernel, C::SMEM, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = tiles_of(A.N, A.B, A.Hq / A.H);
     const int64_t limit = (int64_t)A.max_pages * A.page, seen = A.window > 0 ? std::min(limit, A.window + A.N / A.B) : limit;

@@ -418,33 +418,28 @@ def lsa_lightning_topk_step(q_step, w_step, hot_K, hot_scale, idx, count, seq_of
 # A decode step makes these calls once per layer, so the checks are written to cost little: one pass of
 # cheap conditions; what a failed one has to say is worked out after it has failed.
 
-def _placed(what, tensors, strided):
-    """All tensors on one CUDA device and contiguous (those in `strided`: on it); returns the device's index.
-    tensors, strided: tuples of (name, tensor or None) pairs, the first of `strided` given."""
-    dev = -1
-    for name, t in strided:
+def _placed(what, names, tensors, strided):
+    """All tensors (None: not given) on one CUDA device and contiguous, but for the first `strided` of them,
+    which need not be contiguous; returns the device's index."""
+    dev = tensors[0].get_device()
+    for i, t in enumerate(tensors):
+        if t is not None and (t.get_device() != dev or not (i < strided or t.is_contiguous())):
+            dev = -2
+            break
+    if dev >= 0:
+        return dev
+    first = None
+    for i, (name, t) in enumerate(zip(names, tensors)):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError("device tensor expected (got a CPU tensor)")
-        if dev < 0:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the others on cuda:{dev}")
-    for name, t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError("device tensor expected (got a CPU tensor)")
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the others on cuda:{dev}")
-        if not t.is_contiguous():
+        first = t.device if first is None else first
+        if t.device != first:
+            raise ValueError(f"{what}: {name} is on {t.device}, the others on {first}")
+        if i >= strided and not t.is_contiguous():
             raise ValueError("tensors passed to the LSA library must be contiguous")
-    return dev
+    raise ValueError("device tensor expected")
 
 
 def _rows(name, t, D):
@@ -454,6 +449,8 @@ def _rows(name, t, D):
         raise ValueError(f"{name} must be [N][heads][{D}], got {list(t.shape)}")
     N, h, d = t.shape
     s0, s1, s2 = t.stride()
+    if d == D and s2 == 1 and s1 == d and N > 1 and s0 >= h * d:
+        return N, h, s0
     if d != D:
         raise ValueError(f"{name} must be [N][heads][{D}], got {list(t.shape)}")
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
@@ -512,6 +509,10 @@ def _on(dev, stream, f, *args):
         _check(status)
 
 
+_LSA_KV_APPEND = ("k", "v", "q", "q_offsets", "cache_len", "page_table", "k_cache", "v_cache", "k_scale", "v_scale",
+                  "inv_freq", "q_out")
+
+
 def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale=None, v_scale=None, inv_freq=None,
                   interleaved=False, q=None, q_out=None, stream=None):
     """Rotate the new tokens' keys (and queries) to their positions and write keys and values into the
@@ -542,10 +543,8 @@ def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_sc
         if inv_freq.dtype != torch.float32:
             _need(torch.float32, inv_freq=inv_freq)
         rot = 2 * inv_freq.numel()
-    dev = _placed("lsa_kv_append",
-                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("inv_freq", inv_freq),
-                   ("q_out", q_out)), (("k", k), ("v", v), ("q", q)))
+    dev = _placed("lsa_kv_append", _LSA_KV_APPEND, (k, v, q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale,
+                  inv_freq, q_out), 3)
     _on(dev, stream, _lib.lsa_kv_append, _ptr(q), sq, k.data_ptr(), sk, v.data_ptr(), sv, DTYPE_CODE[dt],
         q_offsets.data_ptr(), N, B, cache_len.data_ptr(), page_table.data_ptr(), max_pages, _ptr(inv_freq), rot,
         1 if interleaved else 0, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode, _ptr(k_scale),
@@ -573,6 +572,10 @@ def lsa_window_attention_workspace_size(N, B, H_q, H_kv, D) -> int:
     return int(_lib.lsa_window_attention_workspace_size(N, B, H_q, H_kv, D))
 
 
+_LSA_WINDOW_ATTENTION = ("q", "q_offsets", "cache_len", "page_table", "k_cache", "v_cache", "k_scale", "v_scale",
+                         "out", "lse_out", "workspace")
+
+
 def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, out, workspace, window=0, n_sink=0,
                          softmax_scale=None, k_scale=None, v_scale=None, lse_out=None, stream=None):
     """Attention over the paged window cache: a sliding window of `window` tokens (0: no limit) and the
@@ -580,10 +583,8 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
                                                       v_cache, k_scale, v_scale)
     code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
-    dev = _placed("lsa_window_attention",
-                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("out", out), ("lse_out", lse_out),
-                   ("workspace", workspace)), (("q", q),))
+    dev = _placed("lsa_window_attention", _LSA_WINDOW_ATTENTION, (q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale,
+                  out, lse_out, workspace), 1)
     _on(dev, stream, _lib.lsa_window_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode,
         _ptr(k_scale), _ptr(v_scale), window, n_sink, D ** -0.5 if softmax_scale is None else softmax_scale,
@@ -592,6 +593,10 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
 
 def lsa_core_attention_workspace_size(N, B, H_q, H_kv, D, k) -> int:
     return int(_lib.lsa_core_attention_workspace_size(N, B, H_q, H_kv, D, k))
+
+
+_LSA_CORE_ATTENTION = ("q", "q_offsets", "cache_len", "page_table", "k_cache", "v_cache", "topk_idx", "idx", "count",
+                       "seq_offsets", "hot_kv", "win_kv", "out", "lse_out", "workspace")
 
 
 def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, topk_idx, idx, count, seq_offsets, total_S,
@@ -625,11 +630,8 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
             win_kv = None
         elif win_kv.numel() * win_kv.element_size() < B * W * row_bytes:
             _cap_bytes(B * W * row_bytes, win_kv=win_kv)
-    dev = _placed("lsa_core_attention",
-                  (("q_offsets", q_offsets), ("cache_len", cache_len), ("page_table", page_table), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("topk_idx", topk_idx), ("idx", idx), ("count", count),
-                   ("seq_offsets", seq_offsets), ("hot_kv", hot_kv), ("win_kv", win_kv), ("out", out),
-                   ("lse_out", lse_out), ("workspace", workspace)), (("q", q),))
+    dev = _placed("lsa_core_attention", _LSA_CORE_ATTENTION, (q, q_offsets, cache_len, page_table, k_cache, v_cache, topk_idx, idx,
+                  count, seq_offsets, hot_kv, win_kv, out, lse_out, workspace), 1)
     _on(dev, stream, _lib.lsa_core_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), window, n_sink,
         D ** -0.5 if softmax_scale is None else softmax_scale, topk_idx.data_ptr(), k, idx.data_ptr(), count.data_ptr(),
