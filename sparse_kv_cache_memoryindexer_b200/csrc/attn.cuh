@@ -114,7 +114,8 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
     for (int i = lane; i < D; i += 32) qs[i] = load_elem<QT>(A.q, n * A.q_stride + (int64_t)hq * D + i);
     __syncwarp();
     const Span sp = visible_span(pos, A.window, A.n_sink);
-    const int64_t total = sp.total;
+    // (a position behind the page table's end, from a bad length, has no keys: the search does not go there)
+    const int64_t total = sp.sinks + max((int64_t)0, min(pos + 1, (int64_t)A.max_pages * A.page) - sp.lo);
     float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;

@@ -895,8 +895,7 @@ inline int splits_of(int64_t N, int Hq, int H, int sms, int64_t blocks)
 inline size_t parts_bytes(int64_t N, int B, int Hq, int H, int D)
 {
     if (Hq % H) return 0;
-    int z = 1;  // the most that any number of SMs up to 160 asks for
-    for (int sms = 1; sms <= 160; sms++) z = std::max(z, most_splits(N, Hq, H, sms));
+    const int z = most_splits(N, Hq, H, 160);  // (grows with the SMs: enough for any number up to 160)
     if (z == 1) return 0;
     return (size_t)tiles_of(N, B, Hq / H) * H * z * (2 * CTA_ROWS + (size_t)CTA_ROWS * D) * sizeof(float);
 }

@@ -1122,7 +1122,7 @@ lsa_status launch_append(AppendArgs &A, cudaStream_t st)
 lsa_status attention(const char *what, AttnArgs &A, int dt, int cdt, void *workspace, size_t workspace_bytes,
                      size_t need, cudaStream_t st)
 {
-    LSA_REQUIRE(A.q && A.q_offsets && A.cache_len && A.page_table && A.k_cache && A.v_cache && A.out,
+    LSA_REQUIRE(((A.q && A.out) || A.N == 0) && A.q_offsets && A.cache_len && A.page_table && A.k_cache && A.v_cache,
                 "%s: null pointer", what);
     LSA_TRY(check_cache(what, A.N, A.B, A.max_pages, A.Hq, A.H, A.D, A.page, A.n_pages, dt, cdt, A.k_cache, A.v_cache,
                         A.k_scale, A.v_scale));
@@ -1167,8 +1167,8 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
                          lsa_stream_t stream)
 {
     const char *what = "lsa_kv_append";
-    LSA_REQUIRE(k && v && q_offsets && cache_len && page_table && k_cache && v_cache, "%s: null pointer", what);
-    LSA_REQUIRE((q == nullptr) == (q_out == nullptr), "%s: q and q_out are given together", what);
+    LSA_REQUIRE(((k && v) || N == 0) && q_offsets && cache_len && page_table && k_cache && v_cache, "%s: null pointer", what);
+    LSA_REQUIRE((q == nullptr) == (q_out == nullptr) || N == 0, "%s: q and q_out are given together", what);
     LSA_TRY(check_cache(what, N, B, max_pages, H_q, H_kv, D, page_size, n_pages, dt, cdt, k_cache, v_cache, k_scale,
                         v_scale));
     LSA_REQUIRE(rot_dim >= 0 && rot_dim <= D, "%s: rot_dim must be in [0, D]", what);
@@ -1240,7 +1240,7 @@ lsa_status lsa_core_attention(const void *q, int64_t q_stride, lsa_dtype dt, con
                               size_t workspace_bytes, lsa_stream_t stream)
 {
     const char *what = "lsa_core_attention";
-    LSA_REQUIRE(topk_idx && idx && count && seq_offsets && hot_kv, "%s: null pointer", what);
+    LSA_REQUIRE((topk_idx || N == 0) && ((idx && hot_kv) || total_S == 0) && count && seq_offsets, "%s: null pointer", what);
     LSA_REQUIRE(k >= 1 && k <= LSA_MAX_TOPK, "%s: k must be in [1, %d]", what, LSA_MAX_TOPK);
     LSA_REQUIRE(total_S >= 0 && total_S < (int64_t)1 << 31, "%s: total_S must be in [0, 2^31)", what);
     LSA_REQUIRE(W >= 0 && (W == 0) == (win_kv == nullptr), "%s: win_kv is given exactly when W > 0", what);

@@ -513,3 +513,27 @@ def check_signed(case, out, lse):
                 bo, bl = ao.attend_bounds(o, A, abs(mag), K.shape[0], case.D, case.dt, p_dtype)
                 assert ((out[at, hq] - o).abs() <= bo).all(), (b, i, hq)
                 assert abs(float(lse[at, hq]) - l_) <= bl, (b, i, hq)
+
+
+def test_no_tokens_and_no_entries(m):
+    """N = 0 (empty tensors) does nothing; without a single fetched entry the fresh ones still count."""
+    c = Case([0, 0], [30, 4], 2, 4, 64, 16)
+    d = c.cuda()
+    call(m, c, d)
+    c = Case([1, 1], [30, 4], 2, 16, 64, 16, window=20).add_topk(8, [0, 0], [0, 0], 5)
+    run(m, c)
+    m.lsa_check_device()
+
+
+def test_bad_length_with_nan_ends(m):
+    """A length far behind the page table, on rows that come out as NaN: flagged, and the way out for such rows
+    does not walk positions that have no page."""
+    from sparse_kv_cache_memoryindexer_b200 import LSAError
+    for n in (3, 40):
+        c = Case([n], [100], 1, 8, 64, 16)
+        d = c.cuda()
+        d["v_cache"][:] = math.nan
+        d["cache_len"][0] = 2000000000
+        call(m, c, d)
+        with pytest.raises(LSAError, match="count"):
+            m.lsa_check_device()

@@ -178,3 +178,12 @@ def test_binding_rejects_small_buffers_and_types():
         call(win_kv=torch.zeros((2, 4, 500), dtype=torch.uint8))
     with pytest.raises(ValueError, match="seq_offsets"):
         call(seq_offsets=torch.zeros(2, dtype=torch.int64))
+
+
+def test_empty_tensors_are_no_work():
+    """An empty tensor has no pointer: with N = 0 none is asked for, and without entries no list or rows are."""
+    assert append(N=0, q=None, k=None, v=None, qo=None)[0] == 0
+    assert window(N=0, q=None, out=None)[0] == 0
+    assert core(N=0, q=None, out=None, topk=None)[0] == 0
+    assert core(N=0, T=0, idx=None, hot=None)[0] == 0
+    assert core(T=5, idx=None)[0] == 1 and core(T=5, hot=None)[0] == 1
