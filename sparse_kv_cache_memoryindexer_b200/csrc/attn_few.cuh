@@ -1,8 +1,8 @@
 // Core attention for few query rows: decode steps, small groups of tokens, every type and head size.
 //
 // A tile is 16 query rows of one sequence and key/value head (rows are token-major, the G = Hq / H heads
-// of a group inside a token); its keys come in chunks of 16 positions, aligned, so a chunk lies in one
-// page and its 16 rows are contiguous.  With so few rows the time goes into reading keys and values once
+// of a group inside a token); its keys come in aligned chunks of 16 positions (E4M3: 32, in two halves), so
+// 16 positions lie in one page and their rows are contiguous.  With so few rows the time goes into reading keys and values once
 // (HBM), so the kernel is built around loads in flight: every warp walks chunks of its own with its own
 // ring of stages (cp.async, 16 bytes a lane), the 16 rows of the tile in its registers, and never waits
 // for another warp until the tile's end, where the warps' running maxima, sums and outputs are joined.
@@ -37,20 +37,21 @@ namespace few {
 
 constexpr int WARPS = 4;
 constexpr int ROWS = 16;
-constexpr int KEYS = 16;
 constexpr int JOIN_ROWS = 4;       // rows of a tile per CTA of k_attn_join
 
 template <int CT, int D>
 struct Cfg {
     static constexpr int EB = CT == DT_F32 ? 4 : (CT == DT_BF16 ? 2 : 1);
     static constexpr int RB = D * EB;               // bytes of a key or value row
+    static constexpr int KEYS = CT == DT_FP8 ? 32 : 16;  // positions of a chunk: one or two halves of 16
+    static constexpr int KH = KEYS / 16;
     static constexpr int CHUNK = 2 * KEYS * RB;     // keys, then values
     static constexpr int STAGES = 3;
     static constexpr int RING = WARPS * STAGES * CHUNK;
     static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
     static constexpr int NT = D / 8;                // n-tiles of the value product
     static constexpr int QREGS = CT == DT_F32 ? D / 2 : D / 4;  // query fragment registers
-    static constexpr int SMEM = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 16;
+    static constexpr int SMEM = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 32;
 };
 
 // 16-byte piece of a row that holds piece c of row `row`: chosen for each access pattern below so that the
@@ -272,9 +273,9 @@ __device__ __forceinline__ void load_q(const void *const (&row)[2], int c, uint3
     }
 }
 
-// s[j] += query rows . keys 8j .. 8j + 7 of the chunk at shared address kb.
+// s0, s1 += query rows . keys 0 .. 7, 8 .. 15 at shared address kb.
 template <int CT, int D>
-__device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, D>::QREGS], float (&s)[2][4])
+__device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, D>::QREGS], float (&s0)[4], float (&s1)[4])
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     if constexpr (CT == DT_BF16) {
@@ -285,8 +286,8 @@ __device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, 
             uint32_t b[4];
             ldsm4(b, kb + (uint32_t)(row * Cfg<CT, D>::RB + swz<CT, D>(row, 2 * ks + half) * 16));
             const uint32_t a[4] = {q[4 * ks], q[4 * ks + 1], q[4 * ks + 2], q[4 * ks + 3]};
-            mma_bf16(s[0], a, b[0], b[1]);
-            mma_bf16(s[1], a, b[2], b[3]);
+            mma_bf16(s0, a, b[0], b[1]);
+            mma_bf16(s1, a, b[2], b[3]);
         }
     } else if constexpr (CT == DT_FP8) {
 #pragma unroll
@@ -311,7 +312,7 @@ __device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, 
                 for (int j = 0; j < 2; j++) {
                     uint32_t b0, b1;
                     e4m3x4_to_f16x2(w[j][t], b0, b1);
-                    mma_f16(s[j], a, b0, b1);
+                    mma_f16(j ? s1 : s0, a, b0, b1);
                 }
             }
         }
@@ -327,7 +328,7 @@ __device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, 
                     const int ks = 2 * g + t;
                     const float a[4] = {__uint_as_float(q[4 * ks]), __uint_as_float(q[4 * ks + 1]),
                                         __uint_as_float(q[4 * ks + 2]), __uint_as_float(q[4 * ks + 3])};
-                    mma_3xtf32(s[j], a, __uint_as_float(t ? v.z : v.x), __uint_as_float(t ? v.w : v.y));
+                    mma_3xtf32(j ? s1 : s0, a, __uint_as_float(t ? v.z : v.x), __uint_as_float(t ? v.w : v.y));
                 }
             }
         }
@@ -336,12 +337,12 @@ __device__ __forceinline__ void scores(uint32_t kb, const uint32_t (&q)[Cfg<CT, 
 
 // acc += p (16 rows x 16 keys, as the score product leaves them) . values at shared address vb.
 template <int CT, int D>
-__device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], float (&acc)[Cfg<CT, D>::NT][4])
+__device__ __forceinline__ void values(uint32_t vb, const float (&p0)[4], const float (&p1)[4], float (&acc)[Cfg<CT, D>::NT][4])
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     if constexpr (CT == DT_BF16) {
-        const uint32_t a[4] = {pack_b16x2(p[0][0], p[0][1]), pack_b16x2(p[0][2], p[0][3]), pack_b16x2(p[1][0], p[1][1]),
-                               pack_b16x2(p[1][2], p[1][3])};
+        const uint32_t a[4] = {pack_b16x2(p0[0], p0[1]), pack_b16x2(p0[2], p0[3]), pack_b16x2(p1[0], p1[1]),
+                               pack_b16x2(p1[2], p1[3])};
         const int row = lane & 15;
 #pragma unroll
         for (int t = 0; t < D / 16; t++) {  // keys 0-7, 8-15 of dims 16t .. + 7, then of dims 16t + 8 .. + 15
@@ -351,8 +352,8 @@ __device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], floa
             mma_bf16(acc[2 * t + 1], a, b[2], b[3]);
         }
     } else if constexpr (CT == DT_FP8) {
-        const uint32_t a[4] = {pack_f16x2(p[0][0], p[0][1]), pack_f16x2(p[0][2], p[0][3]), pack_f16x2(p[1][0], p[1][1]),
-                               pack_f16x2(p[1][2], p[1][3])};
+        const uint32_t a[4] = {pack_f16x2(p0[0], p0[1]), pack_f16x2(p0[2], p0[3]), pack_f16x2(p1[0], p1[1]),
+                               pack_f16x2(p1[2], p1[3])};
 #pragma unroll
         for (int blk = 0; blk < D / 32; blk++) {
             uint32_t w[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of dims 32 blk + 4r .. + 3
@@ -375,7 +376,7 @@ __device__ __forceinline__ void values(uint32_t vb, const float (&p)[2][4], floa
     } else {
 #pragma unroll
         for (int j = 0; j < 2; j++) {  // k-step j: slots c, c + 4 are keys 8j + 2c, + 1
-            const float a[4] = {p[j][0], p[j][2], p[j][1], p[j][3]};
+            const float a[4] = {j ? p1[0] : p0[0], j ? p1[2] : p0[2], j ? p1[1] : p0[1], j ? p1[3] : p0[3]};
 #pragma unroll
             for (int blk = 0; blk < D / 32; blk++) {
                 const int row = 8 * j + 2 * c;
@@ -462,7 +463,7 @@ __device__ __forceinline__ void find_rows(const AttnArgs &A, int b, int n, int f
 // --------------------------------------------------------------------------------------- the work
 
 // What the tiles of one sequence share.  Chunks are numbered [first tokens][window]: chunk u < sc is positions
-// 16 u .., the others 16 (wc0 + u - sc) .., up to `chunks`; then the chunks of the Top-k list.
+// KEYS u .., the others KEYS (wc0 + u - sc) .., up to `chunks`; then the chunks of the Top-k list.
 struct Seq {
     int off, n;     // first query token, query tokens
     int len;        // tokens before this call's
@@ -474,7 +475,7 @@ struct Seq {
 
 __device__ __forceinline__ int tiles_per_token(const AttnArgs &A) { return (A.Hq / A.H + ROWS - 1) / ROWS; }
 
-template <bool CORE>
+template <bool CORE, int KEYS>
 __device__ __forceinline__ Seq load_seq(const AttnArgs &A, int b)
 {
     Seq s = {};
@@ -502,7 +503,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &A, int b)
     s.wc0 = (int)(first.lo / KEYS);
     s.sc = min((int)((first.sinks + KEYS - 1) / KEYS), s.wc0);
     const int wend = last < 0 ? 0 : last / KEYS + 1;
-    s.sc = min(s.sc, limit / KEYS);
+    s.sc = min(s.sc, (limit + KEYS - 1) / KEYS);
     s.chunks = s.sc + max(0, wend - s.wc0);
     s.total = max(1, s.chunks + (CORE ? (A.k + KEYS - 1) / KEYS : 0));  // (a tile without keys still writes its rows)
     return s;
@@ -568,7 +569,8 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     uint8_t *ring = smem + warp * C::STAGES * C::CHUNK;
     const uint32_t ring_a = (uint32_t)__cvta_generic_to_shared(ring);
     float *ml = (float *)(smem + C::RING);
-    struct Meta { float ks, vs; uint32_t live, pad; };
+    constexpr int KEYS = C::KEYS, KH = C::KH;
+    struct Meta { float sc[2][2]; uint32_t live, pad[3]; };  // key and value scale of each half; which keys are there
     Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
     const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
 
@@ -616,9 +618,9 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
 
-    // A chunk's 16 rows are RB pieces of 16 bytes for the keys and as many for the values; piece lane + 32 x goes to
-    // lane.  The swizzle repeats every 8 rows, i.e. every REP values of x.
-    constexpr int XS = C::RB / 32, REP = C::RB >= 64 ? C::RB / 64 : 1, PR = C::RB / 16;
+    // 16 rows are RB pieces of 16 bytes for the keys and as many for the values; piece lane + 32 x goes to lane, and
+    // XH values of x are a half of a chunk.  The swizzle repeats every 8 rows, i.e. every REP values of x.
+    constexpr int XH = C::RB / 32, REP = C::RB >= 64 ? C::RB / 64 : 1, PR = C::RB / 16;
     uint32_t so[REP];
 #pragma unroll
     for (int x = 0; x < REP; x++) {
@@ -632,44 +634,54 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         if (i >= count) return -1;
         const int u = chunk_of(i);
         if (CORE && u >= s.chunks) return entries[(u - c0) * KEYS + (lane & 15)];
-        return __ldg(A.page_table + (int64_t)b * A.max_pages + (pos_of(u) >> A.page_shift));
+        // (lanes 0-15 for the first half, the others for the second; its page may lie behind the table's end, unseen)
+        const int at = (pos_of(u) + (KH > 1 ? lane & 16 : 0)) >> A.page_shift;
+        return __ldg(A.page_table + (int64_t)b * A.max_pages + (KH > 1 ? min(at, A.max_pages - 1) : at));
     };
     // start the loads of the CTA's i-th chunk (warp w takes w, w + WARPS, ..)
     auto issue = [&](int i, int stage, int32_t found) {
         const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
         const int u = chunk_of(i);
         if (!CORE || u < s.chunks) {
-            const int p0 = pos_of(u);
-            int page = found;
-            if (page < 0 || page >= A.n_pages) {
-                if (lane == 0) flag(ERRF_PAGE);
-                page = -1;
-            }
-            const int64_t ph = (int64_t)max(page, 0) * A.H + h;
-            const int64_t byte = ((ph << A.page_shift) + (p0 & ((1 << A.page_shift) - 1))) * C::RB + lane * 16;
-            const uint8_t *kp = (const uint8_t *)A.k_cache + byte, *vp = (const uint8_t *)A.v_cache + byte;
-            if (page >= 0 && p0 + KEYS - 1 <= t.p_hi && (p0 >= low || p0 + KEYS <= A.n_sink)) {
+            uint32_t live = 0;
 #pragma unroll
-                for (int x = 0; x < XS; x++) cp_async16(kb + dst(x), kp + 512 * x, 16);
-#pragma unroll
-                for (int x = 0; x < XS; x++) cp_async16(vb + dst(x), vp + 512 * x, 16);
-            } else {  // keys that no row of the tile sees come in as zeros
-#pragma unroll
-                for (int x = 0; x < XS; x++) {
-                    const int pos = p0 + (lane + 32 * x) / PR;
-                    const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
-                    cp_async16(kb + dst(x), see ? kp + 512 * x : (const uint8_t *)A.k_cache, see ? 16 : 0);
-                    cp_async16(vb + dst(x), see ? vp + 512 * x : (const uint8_t *)A.v_cache, see ? 16 : 0);
+            for (int hf = 0; hf < KH; hf++) {
+                const int p0 = pos_of(u) + 16 * hf;
+                int page = KH > 1 ? __shfl_sync(0xffffffffu, found, 16 * hf) : found;
+                if (KH > 1 && (p0 > t.p_hi || (p0 + 15 < low && p0 >= A.n_sink))) {
+                    page = -1;  // (a half that no row sees: its page is not looked at)
+                } else if (page < 0 || page >= A.n_pages) {
+                    if (lane == 0) flag(ERRF_PAGE);
+                    page = -1;
                 }
+                const int64_t ph = (int64_t)max(page, 0) * A.H + h;
+                const int64_t byte = ((ph << A.page_shift) + (p0 & ((1 << A.page_shift) - 1))) * C::RB + lane * 16;
+                const uint8_t *kp = (const uint8_t *)A.k_cache + byte, *vp = (const uint8_t *)A.v_cache + byte;
+                if (page >= 0 && p0 + 15 <= t.p_hi && (p0 >= low || p0 + 16 <= A.n_sink)) {
+#pragma unroll
+                    for (int x = 0; x < XH; x++) cp_async16(kb + dst(hf * XH + x), kp + 512 * x, 16);
+#pragma unroll
+                    for (int x = 0; x < XH; x++) cp_async16(vb + dst(hf * XH + x), vp + 512 * x, 16);
+                } else {  // keys that no row of the tile sees come in as zeros
+#pragma unroll
+                    for (int x = 0; x < XH; x++) {
+                        const int pos = p0 + (lane + 32 * x) / PR;
+                        const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
+                        cp_async16(kb + dst(hf * XH + x), see ? kp + 512 * x : (const uint8_t *)A.k_cache, see ? 16 : 0);
+                        cp_async16(vb + dst(hf * XH + x), see ? vp + 512 * x : (const uint8_t *)A.v_cache, see ? 16 : 0);
+                    }
+                }
+                if constexpr (CT == DT_FP8) {
+                    if (lane < 2)
+                        cp_async4(meta_a + (uint32_t)stage * 32 + hf * 8 + lane * 4, (lane ? A.v_scale : A.k_scale) + ph, page >= 0 ? 4 : 0);
+                }
+                if (page >= 0) live |= 0xFFFFu << (16 * hf);
             }
-            if constexpr (CT == DT_FP8) {
-                if (lane < 2) cp_async4(meta_a + (uint32_t)stage * 16 + lane * 4, (lane ? A.v_scale : A.k_scale) + ph, page >= 0 ? 4 : 0);
-            }
-            if (lane == 0) meta[stage].live = page >= 0 ? 0xFFFFu : 0u;
+            if (lane == 0) meta[stage].live = live;
         } else {
             const uint32_t live = __ballot_sync(0xffffffffu, found != NO_ROW) & 0xFFFFu;
 #pragma unroll
-            for (int x = 0; x < XS; x++) {
+            for (int x = 0; x < XH; x++) {
                 const int piece = lane + 32 * x, pc = piece % PR;
                 const int32_t row = __shfl_sync(0xffffffffu, found, piece / PR);
                 const uint8_t *p = (row >= 0 ? A.hot_kv + row * A.row_bytes : A.win_kv + (int64_t)~row * A.row_bytes) +
@@ -685,7 +697,12 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     if constexpr (CORE) {
         if (e2 > 0) find_rows(A, b, t.n0, (c0 - s.chunks) * KEYS, e2 * KEYS, entries, (int32_t *)smem, C::RING / 4);
     }
-    float last_vs = 1.f, lv = 0.f, inv_vs = 1.f;
+    float last_vs[KH], lv[KH], inv_vs[KH];
+#pragma unroll
+    for (int hf = 0; hf < KH; hf++) {
+        last_vs[hf] = inv_vs[hf] = 1.f;
+        lv[hf] = 0.f;
+    }
     {
         int32_t f[C::STAGES - 1];  // (the first look-ups together)
 #pragma unroll
@@ -709,33 +726,43 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         const int u = chunk_of(i);
         const bool listed = CORE && u >= s.chunks;
         uint32_t live = meta[stage].live;
-        float ks = 1.f, vs = 1.f;
-        if constexpr (CT == DT_FP8) {
-            ks = meta[stage].ks;
-            vs = meta[stage].vs;
-            if (live && (!good_scale(ks) || !good_scale(vs))) {
-                if (lane == 0) flag(ERRF_SCALE);
-                live = 0;
-            }
-            if (vs != last_vs) {
-                last_vs = vs;
-                lv = vs > 0.f ? log2f(vs) : 0.f;
-                inv_vs = vs > 0.f ? 1.f / vs : 1.f;
+        float ks[KH];
+#pragma unroll
+        for (int hf = 0; hf < KH; hf++) {
+            ks[hf] = 1.f;
+            if constexpr (CT == DT_FP8) {
+                ks[hf] = meta[stage].sc[hf][0];
+                const float vs = meta[stage].sc[hf][1];
+                if ((live >> (16 * hf) & 1) && (!good_scale(ks[hf]) || !good_scale(vs))) {
+                    if (lane == 0) flag(ERRF_SCALE);
+                    live &= ~(0xFFFFu << (16 * hf));
+                }
+                if (vs != last_vs[hf]) {
+                    last_vs[hf] = vs;
+                    lv[hf] = vs > 0.f ? log2f(vs) : 0.f;
+                    inv_vs[hf] = vs > 0.f ? 1.f / vs : 1.f;
+                }
             }
         }
-        float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        scores<CT, D>(kb, q, x);
+        float x[2 * KH][4];
+#pragma unroll
+        for (int j = 0; j < 2 * KH; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[j][e] = 0.f;
+#pragma unroll
+        for (int hf = 0; hf < KH; hf++) scores<CT, D>(kb + hf * 16 * C::RB, q, x[2 * hf], x[2 * hf + 1]);
         const int p0 = pos_of(u);
-        const bool whole = live == 0xFFFFu &&
+        const bool whole = live == (KH > 1 ? 0xFFFFFFFFu : 0xFFFFu) &&
                            (listed || (p0 + KEYS - 1 <= t.p_lo && (A.window == 0 || p0 > t.p_hi - A.window || p0 + KEYS <= A.n_sink)));
-        const float fa = sf[0] * ks, fb = sf[1] * ks;
 #pragma unroll
-        for (int j = 0; j < 2; j++)
+        for (int j = 0; j < 2 * KH; j++) {
+            const float fa = sf[0] * ks[j / 2], fb = sf[1] * ks[j / 2];
 #pragma unroll
-            for (int e = 0; e < 4; e++) x[j][e] = CT == DT_FP8 ? fmaf(x[j][e], e < 2 ? fa : fb, lv) : x[j][e] * (e < 2 ? fa : fb);
+            for (int e = 0; e < 4; e++) x[j][e] = CT == DT_FP8 ? fmaf(x[j][e], e < 2 ? fa : fb, lv[j / 2]) : x[j][e] * (e < 2 ? fa : fb);
+        }
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int j = 0; j < 2 * KH; j++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int key = 8 * j + 2 * c + (e & 1), pos = p0 + key, me = rpos[e >> 1];
@@ -749,6 +776,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
 #pragma unroll
         for (int i2 = 0; i2 < 2; i2++) {
             float mx = fmaxf(fmaxf(x[0][2 * i2], x[0][2 * i2 + 1]), fmaxf(x[1][2 * i2], x[1][2 * i2 + 1]));
+            if constexpr (KH > 1) mx = fmaxf(mx, fmaxf(fmaxf(x[2][2 * i2], x[2][2 * i2 + 1]), fmaxf(x[3][2 * i2], x[3][2 * i2 + 1])));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             const float mn = fmaxf(m[i2], mx);
@@ -756,16 +784,20 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             f[i2] = exp2_fast(m[i2] - ref);
             moved |= mn != m[i2];
             m[i2] = mn;
-            float sum = 0.f;
+            l[i2] *= f[i2];
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int hf = 0; hf < KH; hf++) {
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    float &v = x[j][2 * i2 + e];
-                    v = exp2_fast(v - (ref - C::SHIFT));
-                    sum += v;
-                }
-            l[i2] = fmaf(l[i2], f[i2], sum * inv_vs);
+                for (int j = 2 * hf; j < 2 * hf + 2; j++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float &v = x[j][2 * i2 + e];
+                        v = exp2_fast(v - (ref - C::SHIFT));
+                        sum += v;
+                    }
+                l[i2] = fmaf(sum, inv_vs[hf], l[i2]);
+            }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -777,7 +809,9 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             }
         }
         // (a value scale of zero: the keys have had their share of the softmax sum and add nothing)
-        if (live != 0 && !(CT == DT_FP8 && vs == 0.f)) values<CT, D>(vb, x, acc);
+#pragma unroll
+        for (int hf = 0; hf < KH; hf++)
+            if ((live >> (16 * hf) & 0xFFFFu) && !(CT == DT_FP8 && last_vs[hf] == 0.f)) values<CT, D>(vb + hf * 16 * C::RB, x[2 * hf], x[2 * hf + 1], acc);
         __syncwarp();
         stage = stage + 1 == C::STAGES ? 0 : stage + 1;
         fill = fill + 1 == C::STAGES ? 0 : fill + 1;
@@ -923,11 +957,11 @@ __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) {
 // CTA whose range holds chunk x.
 __device__ __forceinline__ int cta_of(int64_t total, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
 
-// CTAs that share the work: no more than leave MIN_CHUNKS to each.
-constexpr int MIN_CHUNKS = 2 * WARPS;
+// CTAs that share the work: no more than leave 128 keys to each.
+template <int KEYS>
 __device__ __forceinline__ int sharing_ctas(int64_t total, int grid)
 {
-    const int64_t c = total / MIN_CHUNKS;
+    const int64_t c = total / (128 / KEYS);
     return c < 1 ? 1 : (c < grid ? (int)c : grid);
 }
 
@@ -957,7 +991,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
         __syncthreads();
         const int b = found;
         if (b < 0) return;  // (the whole cluster)
-        const Seq s = load_seq<CORE>(A, b);
+        const Seq s = load_seq<CORE, Cfg<CT, D>::KEYS>(A, b);
         const int64_t tile = x - (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b);
         if (tile >= s.tiles) return;
         const int u0 = (int)((int64_t)s.total * z / Z), u1 = (int)((int64_t)s.total * (z + 1) / Z);
@@ -968,10 +1002,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
         int64_t total = 0, mine = 0, before = 0;  // (of the last group of sequences: the only one up to 128)
         for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
             const int b = b0 + threadIdx.x;
-            mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
+            mine = b < A.B ? seq_cost(A, load_seq<CORE, Cfg<CT, D>::KEYS>(A, b)) : 0;
             total += block_scan(mine, sums, before);
         }
-        const int ctas = sharing_ctas(total, gridDim.x);
+        const int ctas = sharing_ctas<Cfg<CT, D>::KEYS>(total, gridDim.x);
         if (total == 0 || (int)blockIdx.x >= ctas) return;
         int64_t x = range_start(total, blockIdx.x, ctas);
         const int64_t end = range_start(total, blockIdx.x + 1, ctas);
@@ -980,7 +1014,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
             int64_t base = 0;
             for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
                 const int b = b0 + threadIdx.x;
-                mine = b < A.B ? seq_cost(A, load_seq<CORE>(A, b)) : 0;
+                mine = b < A.B ? seq_cost(A, load_seq<CORE, Cfg<CT, D>::KEYS>(A, b)) : 0;
                 const int64_t sum = block_scan(mine, sums, before);
                 before += base;
                 if (base + sum > x) {
@@ -1000,12 +1034,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<CT, D>) k_attn_few(con
         int b = found;
         if (b < 0) return;
         int64_t seq_start = found_before;
-        Seq s = load_seq<CORE>(A, b);
+        Seq s = load_seq<CORE, Cfg<CT, D>::KEYS>(A, b);
         while (x < end) {
             while (x >= seq_start + seq_cost(A, s)) {
                 seq_start += seq_cost(A, s);
                 if (++b >= A.B) return;
-                s = load_seq<CORE>(A, b);
+                s = load_seq<CORE, Cfg<CT, D>::KEYS>(A, b);
             }
             const int64_t rel = x - seq_start;
             const int64_t item = rel / s.total;
@@ -1038,7 +1072,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     for (int b0 = 0; b0 < A.B; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         Seq s = {};
-        if (b < A.B) s = load_seq<CORE>(A, b);
+        if (b < A.B) s = load_seq<CORE, Cfg<CT, D>::KEYS>(A, b);
         const bool mine = s.n > 0 && (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b) <= x;
         if (mine) atomicMax(&found, b);
         int64_t before;
@@ -1050,10 +1084,10 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     pdl_wait();  // (before any return: this launch must not end before the one whose parts it joins)
     const int b = found;
     if (b < 0) return;
-    const Seq s = load_seq<CORE>(A, b);
+    const Seq s = load_seq<CORE, Cfg<CT, D>::KEYS>(A, b);
     const int64_t tile = x - (CORE ? (int64_t)s.off * tiles_per_token(A) : (int64_t)s.off * G / ROWS + b);
     if (tile >= s.tiles) return;
-    const int h = blockIdx.y, ctas = sharing_ctas(total, split_grid);
+    const int h = blockIdx.y, ctas = sharing_ctas<Cfg<CT, D>::KEYS>(total, split_grid);
     const int64_t start = found_before + (tile * A.H + h) * s.total;
     const int c0 = cta_of(total, start, ctas), c1 = cta_of(total, start + s.total - 1, ctas);
     if (c0 == c1) return;  // written whole
@@ -1100,13 +1134,14 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
 constexpr int SPLIT_CTAS = 3 * 148;
 inline size_t parts_bytes(int D) { return (size_t)2 * SPLIT_CTAS * (2 * ROWS + (size_t)ROWS * D) * sizeof(float); }
 
-// Tiles of at most this many chunks go to clusters, where these are few enough to run at once.
-constexpr int64_t CLUSTER_CHUNKS = 256;
+// Tiles of at most this many keys go to clusters, where these are few enough to run at once.
+constexpr int64_t CLUSTER_KEYS = 4096;
 
 template <int QT, int CT, int D, bool CORE>
 cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st, int *launches)
 {
     using C = Cfg<CT, D>;
+    constexpr int KEYS = C::KEYS;
     float *parts = (float *)workspace;
     const int G = A.Hq / A.H, tpt = (G + ROWS - 1) / ROWS;
     const int64_t tiles = CORE ? A.N * tpt : A.N * G / ROWS + A.B;
@@ -1122,13 +1157,13 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     const int per_sm = std::max(1, std::min(CTAS_PER_SM<CT, D>, (int)(227 * 1024 / (smem + 1024))));
     cudaLaunchAttribute attr[1];
     cudaError_t e;
-    if (chunks <= CLUSTER_CHUNKS) {
+    if (chunks * KEYS <= CLUSTER_KEYS) {
         // as many CTAs a tile as leave each one chunk a warp and run at once
         int Z = 1;
         while (Z < 8 && 2 * Z * WARPS <= chunks + WARPS - 1 && 2 * Z * likely * A.H <= per_sm * sms) Z *= 2;
         // (not where the last of several waves would leave more than a quarter of the CTAs' time unused)
         const int64_t ctas = Z * likely * A.H, slots = (int64_t)per_sm * sms;
-        if (chunks <= 64 || ctas <= slots || 4 * ctas >= 3 * ((ctas + slots - 1) / slots) * slots) {
+        if (chunks * KEYS <= 1024 || ctas <= slots || 4 * ctas >= 3 * ((ctas + slots - 1) / slots) * slots) {
             auto kernel = k_attn_few<QT, CT, D, CORE, false>;
             static std::atomic<uint64_t> done{0};
             e = allow_smem(kernel, most_smem, done);
