@@ -18,6 +18,10 @@
 //   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
 //                (the fourth, lo lo, is below 2^-22 of the product).
 //
+// Measured: 32 users over a window of 4096, 8 heads of 128 in bf16: 96 us, 5.4 TB/s, bound by HBM; 8 histories of up
+// to 131071 tokens in E4M3: 225-239 us, 4.5-4.8 TB/s, bound by instruction issue; Top-2048 and a window of 512 for 32
+// users, 64 heads on 2: 41 us, bound by the 16-row tiles, which read a group's rows once for every 16 heads.
+//
 // Work is shared in one of two ways.  Tiles of bounded length (a window, a Top-k list) go to a cluster of up to
 // eight CTAs each, which share its chunks and join their sums through distributed shared memory: one launch.
 // Otherwise the chunks of all tiles of all sequences form one range that the CTAs share evenly, whatever the

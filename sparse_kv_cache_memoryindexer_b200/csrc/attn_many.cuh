@@ -9,8 +9,10 @@
 // core does the other tile's products.  TMEM: S0 S1 O0 O1, 128 columns each; P takes the first 64 of its S.
 // The running maximum is let go stale by up to 2^8: O is brought to a new one only when a row's has grown by
 // more, which after the first blocks is rare, so O stays in TMEM.
-// What bounds it: 128 x 128 exponentials a tile and block (16 a clock and SM) against 2 x 128 x 128 x D
-// multiply-adds (4096 a clock): about the same time at D = 128.
+// What bounds it: a tile's chain of softmax (about 2200 clocks beside the other tile's) and its two products (1000)
+// takes 3500 clocks a block, where the MMAs of both tiles take 2048 (2 x 128 x 128 x D multiply-adds each, 4096 a
+// clock) and their exponentials as long.  Two chunks of 4096 and 1900 tokens over a window of 4096, 32 heads of 128:
+// 530-565 us, 870-925 TFLOP/s (the plain form 42 ms); 2048 tokens on an E4M3 history of 14001: 574 us, 880 TFLOP/s.
 //
 // Keys and values come by TMA, one box per page (128-byte swizzle); E4M3 pages come as they are and four warps
 // decode them exactly to f16 tiles (see attn_few.cuh for how a page's scales enter; the probabilities' factor

@@ -22,7 +22,6 @@ enum : unsigned {
     ERRF_COUNT = 4u,    // a fetched count outside [0, S_b]
     ERRF_SCALE = 8u,    // a key scale that is negative or NaN
     ERRF_TIMEOUT = 16u, // a bounded wait inside a pipelined kernel gave up
-    ERRF_PAGE = 32u,    // a page number outside the cache
 };
 
 // One word per device (per loaded copy of this library).

@@ -17,11 +17,14 @@
 // The work is one pass over the data and bound by HBM; a unit is 16 elements of a row (both partners of
 // eight pairs), so no thread needs another's values.  Rows that are stored as they are read go by token
 // (k_kv_append_rows); an E4M3 page and head is one CTA (its scale needs all its new values, held in
-// registers, and nobody else touches the page).  Both kinds of CTA share one launch.
+// registers, and nobody else touches the page).  Both kinds of CTA share one launch.  16384 tokens of 64 + 16 heads of
+// 128 into a bf16 cache: 146 us, 5.4 TB/s; 8 ragged chunks into an E4M3 cache, 32 query heads: 77 us, 3.4 TB/s.
 #pragma once
 #include "common.cuh"
 
 namespace lsa {
+
+constexpr unsigned ERRF_PAGE = 32u;  // device error word (common.cuh): a page number outside the cache
 
 struct AppendArgs {
     const void *q, *k, *v;          // [N][heads][D], rows of a token contiguous
