@@ -388,8 +388,12 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   out          [N][H_q][D] dt; lse_out [N][H_q] fp32 (nullable)
  * Products and sums are fp32; probabilities enter the value product in bf16 (f16 for E4M3 caches).
  * Limits as lsa_kv_append; H_q a multiple of H_kv; max_pages * page_size below 2^31.  Bad lengths,
- * offsets, pages and scales are flagged, their keys left out.
- * Workspace: lsa_window_attention_workspace_size (partial results of keys split over CTAs).
+ * offsets, pages and scales are flagged, their keys left out.  out must not overlap q.
+ * Kernels: tcgen05 for many query rows (bf16 and E4M3 caches, D = 64 or 128), warp MMAs for few; a
+ * rule on the sizes picks the faster, LSA_ATTN_MANY=0 or 1 in the environment takes the one or the
+ * other wherever it can (the same result up to rounding).
+ * Workspace: lsa_window_attention_workspace_size (partial results of keys split over CTAs); it needs
+ * no initial content.  Calls that may run at the same time (streams, graphs) need one each.
  * ---------------------------------------------------------------------------------------- */
 size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D);
 

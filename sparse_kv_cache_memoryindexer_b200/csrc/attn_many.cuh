@@ -37,7 +37,6 @@ namespace many {
 constexpr int TILE_ROWS = 128;
 constexpr int CTA_ROWS = 256;
 constexpr int BLOCK = 128;        // keys per block
-constexpr int MIN_ROWS = 32;      // query rows a sequence and head (on average) from which this kernel is taken
 constexpr int META = 4;           // blocks whose page data are kept (see the producer)
 
 template <int CT, int D>
@@ -868,36 +867,50 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
 
 inline int64_t tiles_of(int64_t N, int B, int G) { return N * G / CTA_ROWS + B; }
 
-// The most CTAs that may share one tile's keys: what brings the launch to about two for each SM.
-inline int most_splits(int64_t N, int Hq, int H, int sms)
+// Tiles and heads, were the tokens shared evenly by the sequences.
+inline int64_t likely_ctas(int64_t N, int B, int Hq, int H)
 {
-    const int64_t ctas = std::max<int64_t>(N * (Hq / H) / CTA_ROWS, 1) * H;
+    const int64_t rows = std::max<int64_t>(N / B, 1) * (Hq / H);
+    return B * ((rows + CTA_ROWS - 1) / CTA_ROWS) * H;
+}
+
+// The most CTAs that may share one tile's keys: what brings the launch to about two for each SM.
+inline int most_splits(int64_t N, int B, int Hq, int H, int sms)
+{
+    const int64_t ctas = likely_ctas(N, B, Hq, H);
     if (ctas >= sms) return 1;
-    return (int)std::min<int64_t>(16, std::max<int64_t>(1, 2 * (int64_t)sms / ctas));
+    return (int)std::min<int64_t>(64, std::max<int64_t>(1, 2 * (int64_t)sms / ctas));
 }
 
 // CTAs that share one tile's keys, tiles of `blocks` blocks at most: the number with the least time, counted in blocks:
 // the waves of CTAs, each its share of the blocks and about four for its start and end, and about eight for the second
-// launch.  (128 tiles of 34 blocks: 100 us whole, 140 in two parts, which make two waves.)
-inline int splits_of(int64_t N, int Hq, int H, int sms, int64_t blocks)
+// launch.  (128 tiles of 34 blocks: 100 us whole, 140 in two parts, which make two waves.)  least: that time.
+inline int splits_of(int64_t N, int B, int Hq, int H, int sms, int64_t blocks, int64_t *least)
 {
-    const int64_t ctas = std::max<int64_t>(N * (Hq / H) / CTA_ROWS, 1) * H;
+    const int64_t ctas = likely_ctas(N, B, Hq, H);
     int best = 1;
-    int64_t least = INT64_MAX;
-    for (int z = 1; z <= most_splits(N, Hq, H, sms); z++) {
+    *least = INT64_MAX;
+    for (int z = 1; z <= most_splits(N, B, Hq, H, sms); z++) {
         const int64_t t = (ctas * z + sms - 1) / sms * ((blocks + z - 1) / z + 4) + (z > 1 ? 8 : 0);
-        if (t < least) {
-            least = t;
+        if (t < *least) {
+            *least = t;
             best = z;
         }
     }
     return best;
 }
 
+// Keys that a tile sees at most, were the tokens shared evenly.
+inline int64_t likely_keys(const AttnArgs &A)
+{
+    const int64_t limit = (int64_t)A.max_pages * A.page;
+    return A.window > 0 ? std::min(limit, A.window + A.N / A.B) : limit;
+}
+
 inline size_t parts_bytes(int64_t N, int B, int Hq, int H, int D)
 {
     if (Hq % H) return 0;
-    const int z = most_splits(N, Hq, H, 160);  // (grows with the SMs: enough for any number up to 160)
+    const int z = most_splits(N, B, Hq, H, 160);  // (grows with the SMs: enough for any number up to 160)
     if (z == 1) return 0;
     return (size_t)tiles_of(N, B, Hq / H) * H * z * (2 * CTA_ROWS + (size_t)CTA_ROWS * D) * sizeof(float);
 }
@@ -917,12 +930,25 @@ inline bool make_cache_map(CUtensorMap *m, const void *ptr, bool fp8, int64_t ro
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether this kernel takes the call: enough rows for its tiles, and what its MMAs and tensor maps can hold.
-inline bool takes(const AttnArgs &A, int cdt)
+// Whether this kernel takes the call: its MMAs and tensor maps can hold it, and it is the faster one.  Estimates in
+// microseconds from measurements at D = 128: the few-row kernel 8 and 1.25 for each 16-key chunk of a 16-row tile that
+// falls on one of the SM's 8 warps, this one 5 and 2.1 (E4M3: 2.7) for each block of its longest CTA.  Measured (few-row
+// kernel against this one, bf16; E4M3): 32 users, window 4096, 8 heads: 16 rows 101 : 242, 77 : 302; 32 rows 183 : 182,
+// 138 : 226; 64 rows 315 : 179, 259 : 221.  One user, 8 heads, window 512, 128 rows: 12 : 18, 13 : 24.  One user, one
+// head, 131072 keys: 64 rows 45 : 51, 47 : 61; 128 rows 62 : 52, 68 : 63.  LSA_ATTN_MANY=0 or 1 in the environment takes
+// the one or the other wherever it can (to check them against one another).
+inline bool takes(const AttnArgs &A, int cdt, int sms)
 {
     if (cdt == DT_F32 || A.k > 0 || (A.D != 64 && A.D != 128)) return false;
     if (A.n_pages * A.H * A.page >= (int64_t)1 << 31 || A.H > 65535) return false;
-    return A.N * (A.Hq / A.H) >= (int64_t)A.B * MIN_ROWS && tc_available();
+    const char *env = getenv("LSA_ATTN_MANY");
+    if (env && env[0] == '0') return false;
+    const int64_t rows = std::max<int64_t>(A.N / A.B, 1) * (A.Hq / A.H), keys = likely_keys(A);
+    int64_t blocks;
+    splits_of(A.N, A.B, A.Hq, A.H, sms, keys / BLOCK + 1, &blocks);
+    const double few_us = 8 + 1.25 * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
+    const double many_us = 5 + (cdt == DT_FP8 ? 2.7 : 2.1) * blocks;
+    return ((env && env[0] == '1') || many_us < few_us) && tc_available();
 }
 
 template <int CT, int D>
@@ -938,8 +964,8 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     cudaError_t e = allow_smem(kernel, C::SMEM, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = tiles_of(A.N, A.B, A.Hq / A.H);
-    const int64_t limit = (int64_t)A.max_pages * A.page, seen = A.window > 0 ? std::min(limit, A.window + A.N / A.B) : limit;
-    const int Z = splits_of(A.N, A.Hq, A.H, sms, seen / BLOCK + 1);
+    int64_t least;
+    const int Z = splits_of(A.N, A.B, A.Hq, A.H, sms, likely_keys(A) / BLOCK + 1, &least);
     k_attn_many<CT, D><<<dim3((unsigned)tiles, (unsigned)A.H, (unsigned)Z), C::THREADS, C::SMEM, st>>>(A, km, vm, (float *)workspace);
     ++*launches;
     if (Z == 1) return cudaSuccess;

@@ -1128,6 +1128,11 @@ lsa_status attention(const char *what, AttnArgs &A, int dt, int cdt, void *works
                         A.k_scale, A.v_scale));
     LSA_TRY(check_rows(what, "q", A.q, A.q_stride, A.Hq, A.D, dt));
     LSA_REQUIRE(aligned(A.out, 16), "%s: out must be 16-byte aligned", what);
+    if (A.N > 0) {
+        const uintptr_t q0 = (uintptr_t)A.q, q1 = q0 + (uintptr_t)((A.N - 1) * A.q_stride + (int64_t)A.Hq * A.D) * elem_bytes(dt);
+        const uintptr_t o0 = (uintptr_t)A.out, o1 = o0 + (uintptr_t)(A.N * A.Hq * A.D) * elem_bytes(dt);
+        LSA_REQUIRE(q1 <= o0 || o1 <= q0, "%s: q and out overlap", what);
+    }
     LSA_REQUIRE(A.window >= 0 && A.n_sink >= 0, "%s: window and n_sink must not be negative", what);
     LSA_REQUIRE(A.scale - A.scale == 0.f, "%s: softmax_scale must be finite", what);
     if (!workspace || workspace_bytes < need) return fail(LSA_ERR_WORKSPACE, "%s: workspace needs %zu bytes", what, need);
@@ -1140,7 +1145,7 @@ lsa_status attention(const char *what, AttnArgs &A, int dt, int cdt, void *works
         if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, true>(A, workspace, num_sms(), st, &n);
         else e = few::launch_d<DT_BF16, DT_BF16, true>(A, workspace, num_sms(), st, &n);
     } else {
-        if (many::takes(A, cdt)) {
+        if (many::takes(A, cdt, num_sms())) {
             if (cdt == DT_BF16) e = A.D == 64 ? many::launch<DT_BF16, 64>(A, workspace, num_sms(), st, &n)
                                               : many::launch<DT_BF16, 128>(A, workspace, num_sms(), st, &n);
             else e = A.D == 64 ? many::launch<DT_FP8, 64>(A, workspace, num_sms(), st, &n)

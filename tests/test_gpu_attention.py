@@ -537,3 +537,67 @@ def test_bad_length_with_nan_ends(m):
         call(m, c, d)
         with pytest.raises(LSAError, match="count"):
             m.lsa_check_device()
+
+
+# The kernel for many rows is taken where it is the faster one, which the small cases above are not: here they
+# run on it wherever it can take them (and the large ones on the other).
+
+@pytest.fixture
+def many_rows(monkeypatch):
+    monkeypatch.setenv("LSA_ATTN_MANY", "1")
+
+
+@pytest.fixture
+def few_rows(monkeypatch):
+    monkeypatch.setenv("LSA_ATTN_MANY", "0")
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+@pytest.mark.parametrize("H,Hq,D,page", [(1, 1, 64, 16), (2, 16, 128, 64), (1, 7, 128, 32), (2, 64, 64, 128), (3, 12, 128, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (37, 4), (200, 130), (1, 0)])
+def test_many_rows_chunks(m, many_rows, cdt, H, Hq, D, page, window, sinks):
+    test_chunks(m, BF16, cdt, H, Hq, D, page, window, sinks)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+@pytest.mark.parametrize("H,Hq", [(1, 1), (2, 14), (1, 64), (8, 64)])
+def test_many_rows_one_token(m, many_rows, cdt, H, Hq):
+    test_one_token(m, BF16, cdt, H, Hq)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+def test_many_rows_long_caches(m, many_rows, cdt):
+    test_long_caches_of_unlike_lengths(m, BF16, cdt, 1, 8)
+    test_chunk_on_a_long_history(m, cdt)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+def test_few_rows_kernel_takes_chunks(m, few_rows, cdt):
+    test_chunk_on_a_long_history(m, cdt)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+@pytest.mark.parametrize("n", [1, 3, 70, 300])
+def test_many_rows_unused_slots(m, many_rows, cdt, n):
+    test_what_lies_in_unused_slots_does_not_matter(m, cdt, n)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+def test_many_rows_nan(m, many_rows, cdt):
+    test_a_later_tokens_nan_stays_out_of_earlier_rows(m, cdt)
+
+
+def test_many_rows_bad_data_and_the_rest(m, many_rows):
+    test_strided_queries_and_no_lse(m)
+    test_large_scores_and_scale(m)
+    test_rows_with_nothing_to_see(m)
+    test_bad_data_is_left_out_and_flagged(m)
+    test_zero_scales(m)
+    test_many_sequences(m)
+    test_negative_and_zero_scale(m)
+    test_replayed_graph_follows_the_lengths(m)
+    test_two_streams_with_their_own_workspaces(m)
+    test_the_same_bits_every_time(m)
+    test_pages_past_32_bits(m)
+    test_no_tokens_and_no_entries(m)
+    test_bad_length_with_nan_ends(m)

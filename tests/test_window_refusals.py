@@ -22,14 +22,14 @@ def append(**kw):
 
 def window(**kw):
     a = dict(q=P, qs=1024, dt=BF16, offs=P, N=4, B=2, len=P, table=P, mp=8, Hq=8, H=2, D=128, page=64, np=16, kc=P, vc=P,
-             cdt=BF16, ksc=None, vsc=None, window=0, sink=0, scale=0.1, out=P, lse=None, ws=P, wsb=1 << 40, st=None)
+             cdt=BF16, ksc=None, vsc=None, window=0, sink=0, scale=0.1, out=C.c_void_p(1 << 30), lse=None, ws=P, wsb=1 << 40, st=None)
     a.update(kw)
     return lsa.library().lsa_window_attention(*a.values()), lsa.library().lsa_last_error().decode()
 
 
 def core(**kw):
     a = dict(q=P, qs=1024, dt=BF16, offs=P, N=4, B=2, len=P, table=P, mp=8, Hq=8, H=2, D=128, page=64, np=16, kc=P, vc=P,
-             window=0, sink=0, scale=0.1, topk=P, k=16, idx=P, cnt=P, so=P, T=100, hot=P, rb=1024, win=None, W=0, out=P,
+             window=0, sink=0, scale=0.1, topk=P, k=16, idx=P, cnt=P, so=P, T=100, hot=P, rb=1024, win=None, W=0, out=C.c_void_p(1 << 30),
              lse=None, ws=P, wsb=1 << 40, st=None)
     a.update(kw)
     return lsa.library().lsa_core_attention(*a.values()), lsa.library().lsa_last_error().decode()
@@ -78,7 +78,8 @@ def test_attention_refuses(call):
     for kw, st, msg in ((dict(out=None), 1, "null pointer"), (dict(q=None), 1, "null pointer"), (dict(qs=1000), 1, "q_stride"),
                         (dict(window=-1), 1, "negative"), (dict(sink=-1), 1, "negative"), (dict(scale=math.nan), 1, "finite"),
                         (dict(scale=math.inf), 1, "finite"), (dict(ws=None), 5, "workspace needs"), (dict(wsb=16), 5, "workspace needs"),
-                        (dict(ws=C.c_void_p((1 << 20) + 16)), 1, "256-byte"), (dict(out=C.c_void_p((1 << 20) + 4)), 1, "16-byte")):
+                        (dict(ws=C.c_void_p((1 << 20) + 16)), 1, "256-byte"), (dict(out=C.c_void_p((1 << 20) + 4)), 1, "16-byte"),
+                        (dict(out=P), 1, "overlap"), (dict(out=C.c_void_p((1 << 20) + 2048)), 1, "overlap")):
         got, text = call(**kw)
         assert got == st and msg in text, (kw, got, text)
 
@@ -103,7 +104,7 @@ def test_workspace_sizes():
     assert w(64, 1, 8, 1, 128) >= 2 * 256 * 130 * 4
     assert w(-1, 1, 8, 1, 128) == 0 and w(1, 0, 8, 1, 128) == 0 and c(1, 1, 0, 1, 128, 4) == 0
     # the size never depends on what the keys are, and stays bounded for long calls
-    assert w(1 << 20, 16, 64, 8, 128) < 64 << 20
+    assert w(1 << 20, 16, 64, 8, 128) < 64 << 20 and w(64, 1, 64, 1, 128) < 64 << 20
 
 
 def tensors(**over):
