@@ -311,70 +311,72 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    // the query rows, D / 8 lanes a row, into the swizzled tiles; their addresses first, a row a thread (in the space of
-    // the first key tile)
-    int64_t *row_at = (int64_t *)(base + C::OFF_K);
-    for (int r = tid; r < CTA_ROWS; r += C::THREADS) {
-        int64_t n, pos;
-        int g;
-        row_of(A, j, min(r, j.rows - 1), n, pos, g);
-        row_at[r] = r < j.rows ? n * A.q_stride + (int64_t)(h * G + g) * D : -1;
-    }
-    __syncthreads();
-    constexpr int PIECES = CTA_ROWS * (D / 8);
-    auto q_at = [&](int i) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        return C::OFF_Q + (uint32_t)(r >> 7) * C::TILE_BYTES + (uint32_t)(c >> 3) * 16384u + train_tc::sw128(r & 127, c & 7);
-    };
-    if constexpr (!FP8) {
-        for (int i = tid; i < PIECES; i += C::THREADS) {
-            const int64_t from = row_at[i / (D / 8)];
-            few::cp_async16(sbase + q_at(i), (const __nv_bfloat16 *)A.q + (from < 0 ? 0 : from + (i % (D / 8)) * 8), from < 0 ? 0 : 16);
-        }
-        few::cp_commit();
-        few::cp_wait<0>();
-        if (A.scale < 0.f) {  // the scores' factor is |scale|: the sign goes to the query
-#pragma unroll 1
-            for (int i = tid; i < PIECES; i += C::THREADS) {
-                uint4 *p = (uint4 *)(base + q_at(i));
-                *p = make_uint4(p->x ^ 0x80008000u, p->y ^ 0x80008000u, p->z ^ 0x80008000u, p->w ^ 0x80008000u);
-            }
-        }
-    } else {
-        // f16 by a power of two of the row's own: its largest element comes to [2^8, 2^9)
-        uint4 v[PIECES / C::THREADS];
-#pragma unroll
-        for (int k = 0; k < PIECES / C::THREADS; k++) {
-            const int i = tid + k * C::THREADS;
-            const int64_t from = row_at[i / (D / 8)];
-            v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (from >= 0) v[k] = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + from) + i % (D / 8));
-        }
-#pragma unroll
-        for (int k = 0; k < PIECES / C::THREADS; k++) {
-            const int i = tid + k * C::THREADS;
-            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            float mx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-#pragma unroll
-            for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            int e = 8 - ((int)(__float_as_uint(mx) >> 23) - 127);
-            e = e > 120 ? 120 : (e < -120 ? -120 : e);
-            const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), A.scale);  // (the scores' factor is |scale|)
-            if (i % (D / 8) == 0) qfac[i / (D / 8)] = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int x2 = 0; x2 < 4; x2++)
-                w[x2] = few::pack_f16x2(__uint_as_float(w[x2] << 16) * up, __uint_as_float(w[x2] & 0xFFFF0000u) * up);
-            *(uint4 *)(base + q_at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-    fence_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    // the query rows, D / 8 lanes a row, into the swizzled tiles, by every warp but the producer's, which starts its loads
+    if (warp != 8) {
+        constexpr int STAGERS = C::THREADS - 32;
+        const int st = tid < 256 ? tid : tid - 32;
+        auto row_at = [&](int r) -> int64_t {
+            const int R = j.row0 + r;
+            return r < j.rows ? (j.off + R / G) * A.q_stride + (int64_t)(h * G + R % G) * D : -1;
+        };
+        constexpr int PIECES = CTA_ROWS * (D / 8);
+        auto q_at = [&](int i) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            return C::OFF_Q + (uint32_t)(r >> 7) * C::TILE_BYTES + (uint32_t)(c >> 3) * 16384u + train_tc::sw128(r & 127, c & 7);
+        };
+        if constexpr (!FP8) {
+            for (int i = st; i < PIECES; i += STAGERS) {
+                const int64_t from = row_at(i / (D / 8));
+                few::cp_async16(sbase + q_at(i), (const __nv_bfloat16 *)A.q + (from < 0 ? 0 : from + (i % (D / 8)) * 8), from < 0 ? 0 : 16);
+            }
+            few::cp_commit();
+            few::cp_wait<0>();
+            if (A.scale < 0.f) {  // the scores' factor is |scale|: the sign goes to the query
+#pragma unroll 1
+                for (int i = st; i < PIECES; i += STAGERS) {
+                    uint4 *p = (uint4 *)(base + q_at(i));
+                    *p = make_uint4(p->x ^ 0x80008000u, p->y ^ 0x80008000u, p->z ^ 0x80008000u, p->w ^ 0x80008000u);
+                }
+            }
+        } else {
+            // f16 by a power of two of the row's own: its largest element comes to [2^8, 2^9)
+            constexpr int EACH = (PIECES + STAGERS - 1) / STAGERS;  // (whole warps reach or miss the last one: D / 8 lanes a row)
+            uint4 v[EACH];
+#pragma unroll
+            for (int k = 0; k < EACH; k++) {
+                const int i = st + k * STAGERS;
+                const int64_t from = i < PIECES ? row_at(i / (D / 8)) : -1;
+                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (from >= 0) v[k] = __ldg((const uint4 *)((const __nv_bfloat16 *)A.q + from) + i % (D / 8));
+            }
+#pragma unroll
+            for (int k = 0; k < EACH; k++) {
+                const int i = st + k * STAGERS;
+                if (i >= PIECES) break;
+                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                float mx = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+#pragma unroll
+                for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                int e = 8 - ((int)(__float_as_uint(mx) >> 23) - 127);
+                e = e > 120 ? 120 : (e < -120 ? -120 : e);
+                const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), A.scale);  // (the scores' factor is |scale|)
+                if (i % (D / 8) == 0) qfac[i / (D / 8)] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int x2 = 0; x2 < 4; x2++)
+                    w[x2] = few::pack_f16x2(__uint_as_float(w[x2] << 16) * up, __uint_as_float(w[x2] & 0xFFFF0000u) * up);
+                *(uint4 *)(base + q_at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        fence_async();
+        asm volatile("bar.sync 1, %0;" ::"n"(STAGERS) : "memory");
+    }
     auto block_pos = [&](int i) -> int64_t { return (int64_t)(i < j.sb ? i : j.wb0 + (i - j.sb)) * BLOCK; };
 
     if (warp < 8) {
@@ -547,202 +549,202 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
     } else if (warp < 12) {
         setmaxnreg_dec<C::REGS_ISSUE>();
         if (warp == 8) {
-        // ------------------------------------------------------- producer: lane x has page x of the block
-        const int per_block = BLOCK / A.page;
-        const uint32_t page_bytes = (uint32_t)A.page * (FP8 ? D : 128);  // of one box
-        const int boxes = FP8 ? 1 : NB;
-        int issued = 0;
-        int specials = 0;
-        bool special = false;
-        // Page numbers are read two blocks ahead, an E4M3 page's scales one: with the reads in the loop's way a block of
-        // an E4M3 history took 6600 clocks.
-        auto read_page = [&](int i) -> int32_t {  // (-1: no query sees it, or there is no such block)
-            if (i >= nb) return -1;
-            const int64_t pa = block_pos(i0 + i) + (int64_t)lane * A.page;
-            if (lane >= per_block || pa > j.last || (pa + A.page <= j.low && pa >= A.n_sink)) return -1;
-            const int32_t p = __ldg(A.page_table + (int64_t)j.b * A.max_pages + pa / A.page);
-            return p < 0 ? -2 : p;  // (-2: seen, and not there)
-        };
-        auto good_page = [&](int32_t p) { return p >= 0 && p < A.n_pages; };
-        auto read_scale = [&](const float *s, int32_t p) { return FP8 && good_page(p) ? __ldg(s + (int64_t)p * A.H + h) : 1.f; };
-        int32_t page1 = read_page(0), page2 = read_page(1);
-        float ks1 = read_scale(A.k_scale, page1), vs1 = read_scale(A.v_scale, page1);
-        for (int i = 0; i < nb; i++) {
-            const int64_t p0 = block_pos(i0 + i);
-            int32_t page = page1;
-            const float ks = ks1, vs = vs1;
-            page1 = page2;
-            page2 = read_page(i + 2);
-            ks1 = read_scale(A.k_scale, page1);
-            vs1 = read_scale(A.v_scale, page1);
-            if (page != -1 && !good_page(page)) {
-                flag(ERRF_PAGE);
-                page = -1;
-            }
-            if (FP8 && page >= 0 && (!good_scale(ks) || !good_scale(vs))) {
-                flag(ERRF_SCALE);
-                page = -1;
-            }
-            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-            const uint32_t bytes = (uint32_t)__popc(there) * page_bytes * boxes;
-            const int y = (int)(((int64_t)max(page, 0) * A.H + h) * A.page);
-            // keys.  (A block's Meta is written once its stage is free, when S of block i - 2 is done: softmax may
-            // still be at i - 2, or i - 3 of the E4M3 path, which runs one block further ahead, but no further back.)
-            if (!wait_warp(FP8 ? kraw_empty : k_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
-            Meta *me = meta + (i & (META - 1));
-            if (lane < per_block) {
-                const float lv = FP8 && page >= 0 && vs > 0.f ? log2f(vs) : 0.f, inv = FP8 && page >= 0 && vs > 0.f ? 1.f / vs : 1.f;
-                for (int k = 0; k < A.page / 16; k++) {
-                    const int at = lane * (A.page / 16) + k;
-                    me->ks[at] = page >= 0 ? ks : 0.f;
-                    me->lv[at] = lv;
-                    me->inv[at] = inv;
+            // ------------------------------------------------------- producer: lane x has page x of the block
+            const int per_block = BLOCK / A.page;
+            const uint32_t page_bytes = (uint32_t)A.page * (FP8 ? D : 128);  // of one box
+            const int boxes = FP8 ? 1 : NB;
+            int issued = 0;
+            int specials = 0;
+            bool special = false;
+            // Page numbers are read two blocks ahead, an E4M3 page's scales one: with the reads in the loop's way a block of
+            // an E4M3 history took 6600 clocks.
+            auto read_page = [&](int i) -> int32_t {  // (-1: no query sees it, or there is no such block)
+                if (i >= nb) return -1;
+                const int64_t pa = block_pos(i0 + i) + (int64_t)lane * A.page;
+                if (lane >= per_block || pa > j.last || (pa + A.page <= j.low && pa >= A.n_sink)) return -1;
+                const int32_t p = __ldg(A.page_table + (int64_t)j.b * A.max_pages + pa / A.page);
+                return p < 0 ? -2 : p;  // (-2: seen, and not there)
+            };
+            auto good_page = [&](int32_t p) { return p >= 0 && p < A.n_pages; };
+            auto read_scale = [&](const float *s, int32_t p) { return FP8 && good_page(p) ? __ldg(s + (int64_t)p * A.H + h) : 1.f; };
+            int32_t page1 = read_page(0), page2 = read_page(1);
+            float ks1 = read_scale(A.k_scale, page1), vs1 = read_scale(A.v_scale, page1);
+            for (int i = 0; i < nb; i++) {
+                const int64_t p0 = block_pos(i0 + i);
+                int32_t page = page1;
+                const float ks = ks1, vs = vs1;
+                page1 = page2;
+                page2 = read_page(i + 2);
+                ks1 = read_scale(A.k_scale, page1);
+                vs1 = read_scale(A.v_scale, page1);
+                if (page != -1 && !good_page(page)) {
+                    flag(ERRF_PAGE);
+                    page = -1;
                 }
-            }
-            uint32_t live = 0, zero = 0;
-            {
-                const uint32_t zs = __ballot_sync(0xffffffffu, page >= 0 && vs == 0.f);
-                for (int k = 0; k < 8; k++) {
-                    const int p = k * 16 / A.page;
-                    live |= (there >> p & 1u) << k;
-                    zero |= (zs >> p & 1u) << k;
+                if (FP8 && page >= 0 && (!good_scale(ks) || !good_scale(vs))) {
+                    flag(ERRF_SCALE);
+                    page = -1;
                 }
-            }
-            if (lane == 0) {
-                me->live = live;
-                me->zero = zero;
-            }
-            __syncwarp();
-            const uint32_t kf = FP8 ? kraw_full : k_full(i & 1);
-            if (lane == 0) mbar_expect_tx(kf, bytes);
-            __syncwarp();
-            if (page >= 0) {
-                const uint32_t dst = sbase + (FP8 ? C::OFF_KRAW : C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES) + (uint32_t)lane * page_bytes;
-                for (int bx = 0; bx < boxes; bx++) tma_load_2d(dst + bx * 16384u, &kmap, 64 * bx, y, kf);
-            }
-            __syncwarp();
-            // values
-            if (!wait_warp(FP8 ? vraw_empty : v_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
-            const uint32_t vdst = sbase + (FP8 ? C::OFF_VRAW : C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES);
-            uint32_t vf = FP8 ? vraw_full : v_full(i & 1);
-            if constexpr (!FP8) {
-                // rows that no query sees must be zero: on pages that are not loaded, and parts of pages that are (those
-                // after they have landed)
-                uint8_t *vt = base + C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES;
-                int gap0, gap1, end;
-                seen_rows(A, j, p0, gap0, gap1, end);
-                auto seen = [&](int row) { return row < end && (row < gap0 || row >= gap1); };
-                auto clear = [&](int from, int to) {
-                    for (int e = 8 * from + lane; e < 8 * to; e += 32)
+                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t bytes = (uint32_t)__popc(there) * page_bytes * boxes;
+                const int y = (int)(((int64_t)max(page, 0) * A.H + h) * A.page);
+                // keys.  (A block's Meta is written once its stage is free, when S of block i - 2 is done: softmax may
+                // still be at i - 2, or i - 3 of the E4M3 path, which runs one block further ahead, but no further back.)
+                if (!wait_warp(FP8 ? kraw_empty : k_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
+                Meta *me = meta + (i & (META - 1));
+                if (lane < per_block) {
+                    const float lv = FP8 && page >= 0 && vs > 0.f ? log2f(vs) : 0.f, inv = FP8 && page >= 0 && vs > 0.f ? 1.f / vs : 1.f;
+                    for (int k = 0; k < A.page / 16; k++) {
+                        const int at = lane * (A.page / 16) + k;
+                        me->ks[at] = page >= 0 ? ks : 0.f;
+                        me->lv[at] = lv;
+                        me->inv[at] = inv;
+                    }
+                }
+                uint32_t live = 0, zero = 0;
+                {
+                    const uint32_t zs = __ballot_sync(0xffffffffu, page >= 0 && vs == 0.f);
+                    for (int k = 0; k < 8; k++) {
+                        const int p = k * 16 / A.page;
+                        live |= (there >> p & 1u) << k;
+                        zero |= (zs >> p & 1u) << k;
+                    }
+                }
+                if (lane == 0) {
+                    me->live = live;
+                    me->zero = zero;
+                }
+                __syncwarp();
+                const uint32_t kf = FP8 ? kraw_full : k_full(i & 1);
+                if (lane == 0) mbar_expect_tx(kf, bytes);
+                __syncwarp();
+                if (page >= 0) {
+                    const uint32_t dst = sbase + (FP8 ? C::OFF_KRAW : C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES) + (uint32_t)lane * page_bytes;
+                    for (int bx = 0; bx < boxes; bx++) tma_load_2d(dst + bx * 16384u, &kmap, 64 * bx, y, kf);
+                }
+                __syncwarp();
+                // values
+                if (!wait_warp(FP8 ? vraw_empty : v_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
+                const uint32_t vdst = sbase + (FP8 ? C::OFF_VRAW : C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES);
+                uint32_t vf = FP8 ? vraw_full : v_full(i & 1);
+                if constexpr (!FP8) {
+                    // rows that no query sees must be zero: on pages that are not loaded, and parts of pages that are (those
+                    // after they have landed)
+                    uint8_t *vt = base + C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES;
+                    int gap0, gap1, end;
+                    seen_rows(A, j, p0, gap0, gap1, end);
+                    auto seen = [&](int row) { return row < end && (row < gap0 || row >= gap1); };
+                    auto clear = [&](int from, int to) {
+                        for (int e = 8 * from + lane; e < 8 * to; e += 32)
 #pragma unroll
-                        for (int bx = 0; bx < NB; bx++) *(uint4 *)(vt + bx * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-                };
-                const uint32_t real = vf;
-                const bool part_seen = lane < per_block && page >= 0 &&
-                                       !(seen(lane * A.page) && seen(lane * A.page + A.page - 1) &&
-                                         (gap0 >= gap1 || gap1 <= lane * A.page || gap0 >= lane * A.page + A.page));
-                special = __any_sync(0xffffffffu, part_seen);
-                if (special) vf = landed;
-                if (live != 0xFFu) {
-                    for (int q = 0; q < per_block; q++)
-                        if (!(there >> q & 1)) clear(q * A.page, (q + 1) * A.page);
-                    fence_async();
+                            for (int bx = 0; bx < NB; bx++) *(uint4 *)(vt + bx * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    };
+                    const uint32_t real = vf;
+                    const bool part_seen = lane < per_block && page >= 0 &&
+                                           !(seen(lane * A.page) && seen(lane * A.page + A.page - 1) &&
+                                             (gap0 >= gap1 || gap1 <= lane * A.page || gap0 >= lane * A.page + A.page));
+                    special = __any_sync(0xffffffffu, part_seen);
+                    if (special) vf = landed;
+                    if (live != 0xFFu) {
+                        for (int q = 0; q < per_block; q++)
+                            if (!(there >> q & 1)) clear(q * A.page, (q + 1) * A.page);
+                        fence_async();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_expect_tx(vf, bytes);
                     __syncwarp();
-                }
-                if (lane == 0) mbar_expect_tx(vf, bytes);
-                __syncwarp();
-                if (page >= 0)
-                    for (int bx = 0; bx < NB; bx++) tma_load_2d(vdst + (uint32_t)lane * page_bytes + bx * 16384u, &vmap, 64 * bx, y, vf);
-                __syncwarp();
-                if (special) {  // (a few blocks of a CTA's: at the ends of the first tokens, the window, the cache)
-                    if (!wait_warp(landed, specials & 1, abort_flag)) break;
-                    clear(gap0, gap1);
-                    clear(end, BLOCK);
-                    fence_async();
+                    if (page >= 0)
+                        for (int bx = 0; bx < NB; bx++) tma_load_2d(vdst + (uint32_t)lane * page_bytes + bx * 16384u, &vmap, 64 * bx, y, vf);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(real);
-                    __syncwarp();
-                    special = false;
-                    specials++;
-                }
-            } else {
-                if (lane == 0) mbar_expect_tx(vf, bytes);
-                __syncwarp();
-                if (page >= 0) tma_load_2d(vdst + (uint32_t)lane * page_bytes, &vmap, 0, y, vf);
-                __syncwarp();
-            }
-            issued = i + 1;
-        }
-        if (*abort_flag && lane == 0) {
-            // let the copies in flight land before the CTA exits (those of the block that broke off among them)
-            for (int i = max(0, issued - 2); i <= min(issued, nb - 1); i++) {
-                if (FP8) {
-                    wait_alone(kraw_full, i & 1);
-                    wait_alone(vraw_full, i & 1);
+                    if (special) {  // (a few blocks of a CTA's: at the ends of the first tokens, the window, the cache)
+                        if (!wait_warp(landed, specials & 1, abort_flag)) break;
+                        clear(gap0, gap1);
+                        clear(end, BLOCK);
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(real);
+                        __syncwarp();
+                        special = false;
+                        specials++;
+                    }
                 } else {
-                    wait_alone(k_full(i & 1), (i >> 1) & 1);
-                    wait_alone(v_full(i & 1), (i >> 1) & 1);
+                    if (lane == 0) mbar_expect_tx(vf, bytes);
+                    __syncwarp();
+                    if (page >= 0) tma_load_2d(vdst + (uint32_t)lane * page_bytes, &vmap, 0, y, vf);
+                    __syncwarp();
                 }
+                issued = i + 1;
             }
-            if (!FP8 && special) wait_alone(landed, specials & 1);
-        }
-        __syncwarp();
+            if (*abort_flag && lane == 0) {
+                // let the copies in flight land before the CTA exits (those of the block that broke off among them)
+                for (int i = max(0, issued - 2); i <= min(issued, nb - 1); i++) {
+                    if (FP8) {
+                        wait_alone(kraw_full, i & 1);
+                        wait_alone(vraw_full, i & 1);
+                    } else {
+                        wait_alone(k_full(i & 1), (i >> 1) & 1);
+                        wait_alone(v_full(i & 1), (i >> 1) & 1);
+                    }
+                }
+                if (!FP8 && special) wait_alone(landed, specials & 1);
+            }
+            __syncwarp();
         } else if (warp == 9) {
-        // ------------------------------------------------------- MMA issuer: one thread from here to the end (the
-        // tensor core waits for it; warp-wide waits and elections cost it about 100 clocks each)
-        if (elect_one()) {
-            bool ok = true;
-            auto score = [&](int t, int i) {
-                const uint32_t q = sbase + C::OFF_Q + (uint32_t)t * C::TILE_BYTES, k = sbase + C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES;
+            // ------------------------------------------------------- MMA issuer: one thread from here to the end (the
+            // tensor core waits for it; warp-wide waits and elections cost it about 100 clocks each)
+            if (elect_one()) {
+                bool ok = true;
+                auto score = [&](int t, int i) {
+                    const uint32_t q = sbase + C::OFF_Q + (uint32_t)t * C::TILE_BYTES, k = sbase + C::OFF_K + (uint32_t)(i & 1) * C::TILE_BYTES;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; kk++) {
-                    const uint32_t o = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-                    mma_bf16(tmem + (uint32_t)t * 128u, sdesc(q + o), sdesc(k + o), C::IDESC_S, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(s_full(t));
-                if (t == 1) mma_commit(k_empty(i & 1));
-            };
-            auto value = [&](int t, int i, int half) {
-                const uint32_t v = sbase + C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES;
+                    for (int kk = 0; kk < D / 16; kk++) {
+                        const uint32_t o = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+                        mma_bf16(tmem + (uint32_t)t * 128u, sdesc(q + o), sdesc(k + o), C::IDESC_S, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(s_full(t));
+                    if (t == 1) mma_commit(k_empty(i & 1));
+                };
+                auto value = [&](int t, int i, int half) {
+                    const uint32_t v = sbase + C::OFF_V + (uint32_t)(i & 1) * C::TILE_BYTES;
 #pragma unroll
-                for (int k2 = 0; k2 < BLOCK / 32; k2++) {
-                    const int kk = half * (BLOCK / 32) + k2;
-                    mma_ts(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + 8u * kk,
-                           train_tc::sdesc_mn(v + 2048u * kk, 16384u, 1024u), C::IDESC_O, (i > 0 || kk > 0) ? 1u : 0u);
-                }
-                if (half == 1) {
-                    mma_commit(o_done(t));
-                    if (t == 1) mma_commit(v_empty(i & 1));
-                }
-            };
-            ok = wait_bar(k_full(0), 0, abort_flag);
-            if (ok) {
-                tc_fence_after();
-                score(0, 0);
-                score(1, 0);
-            }
-            for (int i = 0; i < nb && ok; i++) {
-                const bool more = i + 1 < nb;
-#pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    ok = wait_bar(p_half(t), i & 1, abort_flag) && (t == 1 || wait_bar(v_full(i & 1), (i >> 1) & 1, abort_flag));
-                    if (!ok) break;
+                    for (int k2 = 0; k2 < BLOCK / 32; k2++) {
+                        const int kk = half * (BLOCK / 32) + k2;
+                        mma_ts(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + 8u * kk,
+                               train_tc::sdesc_mn(v + 2048u * kk, 16384u, 1024u), C::IDESC_O, (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    if (half == 1) {
+                        mma_commit(o_done(t));
+                        if (t == 1) mma_commit(v_empty(i & 1));
+                    }
+                };
+                ok = wait_bar(k_full(0), 0, abort_flag);
+                if (ok) {
                     tc_fence_after();
-                    value(t, i, 0);
-                    ok = wait_bar(p_full(t), i & 1, abort_flag) &&
-                         (t == 1 || !more || wait_bar(k_full((i + 1) & 1), ((i + 1) >> 1) & 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    value(t, i, 1);
-                    if (more) score(t, i + 1);
+                    score(0, 0);
+                    score(1, 0);
+                }
+                for (int i = 0; i < nb && ok; i++) {
+                    const bool more = i + 1 < nb;
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        ok = wait_bar(p_half(t), i & 1, abort_flag) && (t == 1 || wait_bar(v_full(i & 1), (i >> 1) & 1, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                        value(t, i, 0);
+                        ok = wait_bar(p_full(t), i & 1, abort_flag) &&
+                             (t == 1 || !more || wait_bar(k_full((i + 1) & 1), ((i + 1) >> 1) & 1, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                        value(t, i, 1);
+                        if (more) score(t, i + 1);
+                    }
+                }
+                if (!ok) {  // whatever was issued ends before TMEM and shared memory go
+                    mma_commit(drained);
+                    wait_alone(drained, 0);
                 }
             }
-            if (!ok) {  // whatever was issued ends before TMEM and shared memory go
-                mma_commit(drained);
-                wait_alone(drained, 0);
-            }
-        }
-        __syncwarp();
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------------- E4M3 pages to f16 tiles (warps 12 .. 15)
@@ -931,11 +933,11 @@ inline bool make_cache_map(CUtensorMap *m, const void *ptr, bool fp8, int64_t ro
 }
 
 // Whether this kernel takes the call: its MMAs and tensor maps can hold it, and it is the faster one.  Estimates in
-// microseconds from measurements at D = 128: the few-row kernel 8 and 1.25 for each 16-key chunk of a 16-row tile that
-// falls on one of the SM's 8 warps, this one 5 and 2.1 (E4M3: 2.7) for each block of its longest CTA.  Measured (few-row
-// kernel against this one, bf16; E4M3): 32 users, window 4096, 8 heads: 16 rows 101 : 242, 77 : 302; 32 rows 183 : 182,
-// 138 : 226; 64 rows 315 : 179, 259 : 221.  One user, 8 heads, window 512, 128 rows: 12 : 18, 13 : 24.  One user, one
-// head, 131072 keys: 64 rows 45 : 51, 47 : 61; 128 rows 62 : 52, 68 : 63.  LSA_ATTN_MANY=0 or 1 in the environment takes
+// microseconds from measurements at D = 128: the few-row kernel 8 and 1.45 (E4M3: 1.12) for each 16-key chunk of a 16-row
+// tile that falls on one of the SM's 8 warps, this one 5 and 1.8 (2.2) for each block of its longest CTA.  Measured (few-row
+// kernel : this one, bf16; E4M3): 32 users, window 4096, 8 heads: 16 rows 98 : 140, 77 : 174; 32 rows 181 : 141,
+// 138 : 175; 64 rows 315 : 141, 259 : 176.  One user, 8 heads, window 512, 128 rows: 12 : 18, 13 : 24.  One user, one
+// head, 131072 keys: 64 rows 45 : 51, 47 : 61; 128 rows 62 : 52, 68 : 64.  LSA_ATTN_MANY=0 or 1 in the environment takes
 // the one or the other wherever it can (to check them against one another).
 inline bool takes(const AttnArgs &A, int cdt, int sms)
 {
@@ -946,8 +948,8 @@ inline bool takes(const AttnArgs &A, int cdt, int sms)
     const int64_t rows = std::max<int64_t>(A.N / A.B, 1) * (A.Hq / A.H), keys = likely_keys(A);
     int64_t blocks;
     splits_of(A.N, A.B, A.Hq, A.H, sms, keys / BLOCK + 1, &blocks);
-    const double few_us = 8 + 1.25 * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
-    const double many_us = 5 + (cdt == DT_FP8 ? 2.7 : 2.1) * blocks;
+    const double few_us = 8 + (cdt == DT_FP8 ? 1.12 : 1.45) * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
+    const double many_us = 5 + (cdt == DT_FP8 ? 2.2 : 1.8) * blocks;
     return ((env && env[0] == '1') || many_us < few_us) && tc_available();
 }
 
