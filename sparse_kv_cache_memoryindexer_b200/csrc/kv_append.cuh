@@ -18,7 +18,8 @@
 // eight pairs), so no thread needs another's values.  Rows that are stored as they are read go by token
 // (k_kv_append_rows); an E4M3 page and head is one CTA (its scale needs all its new values, held in
 // registers, and nobody else touches the page).  Both kinds of CTA share one launch.  16384 tokens of 64 + 16 heads of
-// 128 into a bf16 cache: 146 us, 5.4 TB/s; 8 ragged chunks into an E4M3 cache, 32 query heads: 77 us, 3.4 TB/s.
+// 128 into a bf16 cache: 138 us, 5.7 TB/s; 8 ragged chunks into an E4M3 cache, 32 query heads: 74 us, 3.5 TB/s (bound by
+// instruction issue: the angles of a page's keys are formed for every head).
 #pragma once
 #include "common.cuh"
 
@@ -176,12 +177,10 @@ __device__ __forceinline__ int32_t page_of(const int32_t *page_table, int max_pa
 constexpr int APPEND_TOKENS = 8;  // tokens a CTA takes at most
 
 // Rows that are stored in the type they are read in (queries; keys and values of an fp32 or bf16 cache): a CTA has
-// A.tokens tokens, or a part of one token's rows.  A thread's loads of BATCH units go out together: with one unit at a
-// time a chunk of 16384 tokens ran at 5.3 TB/s.
+// A.tokens tokens, or a part of one token's rows.
 template <int DT, bool KV>
 __device__ __forceinline__ void append_rows(const AppendArgs &A, float2 *cs, SeqOf *slots, int32_t *pages)
 {
-    constexpr int BATCH = 1;
     const int64_t n0 = (int64_t)(blockIdx.x / A.row_ctas_per_token) * A.tokens;
     const int part = blockIdx.x % A.row_ctas_per_token;
     const int many = (int)min((int64_t)A.tokens, A.N - n0);
@@ -210,59 +209,55 @@ __device__ __forceinline__ void append_rows(const AppendArgs &A, float2 *cs, Seq
         pages[threadIdx.x] = page;
     }
     __syncthreads();
-    const int stride = A.row_ctas_per_token * blockDim.x, total = many * units;
-    for (int i0 = part * blockDim.x + threadIdx.x; i0 < total; i0 += BATCH * stride) {
-        float xa[BATCH][8], xb[BATCH][8];
-        void *dst[BATCH];
-        int ra[BATCH], rb[BATCH], turns[BATCH];  // turns: first entry of cs, or -1
-#pragma unroll
-        for (int k = 0; k < BATCH; k++) {
-            const int i = i0 + k * stride;
-            dst[k] = nullptr;
-            if (i >= total) continue;
-            const int t = i / units, row = i % units / upr, u = i % upr;
-            const SeqOf &s = slots[t];
-            if (s.b < 0) continue;  // a row behind the last sequence: left as it is
-            const int64_t n = n0 + t;
-            const void *src;
-            int64_t se, de;
-            bool rot = u < A.rot / 16;
-            if (row < nq) {
-                src = A.q; se = n * A.q_stride + (int64_t)row * A.D;
-                dst[k] = A.q_out; de = (n * A.Hq + row) * A.D;
-            } else {
-                const bool is_v = row >= nq + A.H;
-                const int h = row - nq - (is_v ? A.H : 0);
-                if (pages[t] < 0) continue;
-                src = is_v ? A.v : A.k;
-                se = n * (is_v ? A.v_stride : A.k_stride) + (int64_t)h * A.D;
-                dst[k] = is_v ? A.v_cache : A.k_cache;
-                de = (((int64_t)pages[t] * A.H + h) * A.page + (s.len + (n - s.off)) % A.page) * A.D;
-                rot = rot && !is_v;
-            }
-            turns[k] = rot ? t * half + u : -1;
-            if (rot) unit_runs(A, u, ra[k], rb[k]);
-            else { ra[k] = u * 16; rb[k] = ra[k] + 8; }
-            load_run8<DT>(src, se + ra[k], xa[k]);
-            load_run8<DT>(src, se + rb[k], xb[k]);
-            dst[k] = (char *)dst[k] + de * (DT == DT_F32 ? 4 : 2);
+    // (units of the CTA's tokens one after another; no divisions: a thread's next unit is `stride` on, of this token or a
+    // later one)
+    const int stride = A.row_ctas_per_token * blockDim.x, shift = A.D == 128 ? 3 : (A.D == 64 ? 2 : 1);
+    for (int t = 0, i = part * blockDim.x + threadIdx.x;; i += stride) {
+        while (i >= units && t < many) {
+            i -= units;
+            t++;
         }
-#pragma unroll
-        for (int k = 0; k < BATCH; k++) {
-            if (!dst[k]) continue;
-            if (turns[k] >= 0) {
-                float c[8], s[8];
-#pragma unroll
-                for (int t = 0; t < 8; t++) {
-                    const float2 v = cs[turns[k] + t * (half >> 3)];
-                    c[t] = v.x;
-                    s[t] = v.y;
-                }
-                rotate_unit(A.interleaved, c, s, xa[k], xb[k]);
-            }
-            store_run8<DT>(dst[k], ra[k], xa[k]);
-            store_run8<DT>(dst[k], rb[k], xb[k]);
+        if (t >= many) break;
+        const SeqOf &s = slots[t];
+        if (s.b < 0) continue;  // a row behind the last sequence: left as it is
+        const int row = i >> shift, u = i & (upr - 1);
+        const int64_t n = n0 + t;
+        const void *src;
+        void *dst;
+        int64_t se, de;
+        bool rot = u < A.rot / 16;
+        if (row < nq) {
+            src = A.q; se = n * A.q_stride + (int64_t)row * A.D;
+            dst = A.q_out; de = (n * A.Hq + row) * A.D;
+        } else {
+            const bool is_v = row >= nq + A.H;
+            const int h = row - nq - (is_v ? A.H : 0);
+            if (pages[t] < 0) continue;
+            src = is_v ? A.v : A.k;
+            se = n * (is_v ? A.v_stride : A.k_stride) + (int64_t)h * A.D;
+            dst = is_v ? A.v_cache : A.k_cache;
+            de = (((int64_t)pages[t] * A.H + h) * A.page + ((s.len + (n - s.off)) & (A.page - 1))) * A.D;
+            rot = rot && !is_v;
         }
+        int ra, rb;
+        if (rot) unit_runs(A, u, ra, rb);
+        else { ra = u * 16; rb = ra + 8; }
+        float xa[8], xb[8];
+        load_run8<DT>(src, se + ra, xa);
+        load_run8<DT>(src, se + rb, xb);
+        if (rot) {
+            const float2 *cu = cs + t * half + u;
+            float c[8], sn[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float2 v = cu[e * (half >> 3)];
+                c[e] = v.x;
+                sn[e] = v.y;
+            }
+            rotate_unit(A.interleaved, c, sn, xa, xb);
+        }
+        store_run8<DT>(dst, de + ra, xa);
+        store_run8<DT>(dst, de + rb, xb);
     }
 }
 
