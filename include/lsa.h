@@ -25,7 +25,7 @@
  *   - Errors: a non-LSA_OK status means nothing was launched (or, for LSA_ERR_CUDA, that a
  *     launch failed); lsa_last_error() gives a message for the calling thread.  Kernels that
  *     meet bad data (an index outside its sequence, a count above capacity, a negative or
- *     NaN key scale, decreasing offsets) skip the access and set a device error word, which
+ *     NaN key scale, decreasing offsets, a page outside the cache) skip the access and set a device error word, which
  *     lsa_check_device() reads and clears.  No kernel traps and no kernel waits on another.
  *   - Dtypes: LSA_F32 (IEEE binary32), LSA_BF16 (bfloat16), LSA_FP8_E4M3 (OCP E4M3 with one
  *     fp32 scale per key row: key value = scale * decode(code)).

@@ -419,15 +419,8 @@ def lsa_lightning_topk_step(q_step, w_step, hot_K, hot_scale, idx, count, seq_of
 # cheap conditions; what a failed one has to say is worked out after it has failed.
 
 def _placed(what, names, tensors, strided):
-    """All tensors (None: not given) on one CUDA device and contiguous, but for the first `strided` of them,
-    which need not be contiguous; returns the device's index."""
-    dev = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if t is not None and (t.get_device() != dev or not (i < strided or t.is_contiguous())):
-            dev = -2
-            break
-    if dev >= 0:
-        return dev
+    """What is wrong with the tensors of a call (None: not given), which must be on one CUDA device and
+    contiguous, but for the first `strided` of them, which need not be contiguous."""
     first = None
     for i, (name, t) in enumerate(zip(names, tensors)):
         if t is None:
@@ -439,7 +432,7 @@ def _placed(what, names, tensors, strided):
             raise ValueError(f"{what}: {name} is on {t.device}, the others on {first}")
         if i >= strided and not t.is_contiguous():
             raise ValueError("tensors passed to the LSA library must be contiguous")
-    raise ValueError("device tensor expected")
+    raise ValueError(f"{what}: device tensors expected")
 
 
 def _rows(name, t, D):
@@ -493,14 +486,19 @@ def _cache(what, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_
     return B, page_table.size(1), n_pages, H, page, D, code
 
 
+# (torch.cuda.current_stream() and current_device() without the objects and checks around them)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _on(dev, stream, f, *args):
     """The C call with the tensors' device current, on `stream` (default: that device's current stream)."""
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    if dev == torch._C._cuda_getDevice():
+    st = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == _current_device():
         status = f(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -543,8 +541,21 @@ def lsa_kv_append(k, v, q_offsets, cache_len, page_table, k_cache, v_cache, k_sc
         if inv_freq.dtype != torch.float32:
             _need(torch.float32, inv_freq=inv_freq)
         rot = 2 * inv_freq.numel()
-    dev = _placed("lsa_kv_append", _LSA_KV_APPEND, (k, v, q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale,
-                  inv_freq, q_out), 3)
+    dev = k.get_device()
+    if not (dev >= 0
+            and v.get_device() == dev
+            and (q is None or q.get_device() == dev and q_out.get_device() == dev and q_out.is_contiguous())
+            and q_offsets.get_device() == dev and q_offsets.is_contiguous()
+            and cache_len.get_device() == dev and cache_len.is_contiguous()
+            and page_table.get_device() == dev and page_table.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and (k_scale is None or k_scale.get_device() == dev and k_scale.is_contiguous())
+            and (v_scale is None or v_scale.get_device() == dev and v_scale.is_contiguous())
+            and (inv_freq is None or inv_freq.get_device() == dev and inv_freq.is_contiguous())):
+        _placed("lsa_kv_append", _LSA_KV_APPEND,
+                (k, v, q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale, inv_freq,
+                 q_out), 3)
     _on(dev, stream, _lib.lsa_kv_append, _ptr(q), sq, k.data_ptr(), sk, v.data_ptr(), sv, DTYPE_CODE[dt],
         q_offsets.data_ptr(), N, B, cache_len.data_ptr(), page_table.data_ptr(), max_pages, _ptr(inv_freq), rot,
         1 if interleaved else 0, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode, _ptr(k_scale),
@@ -583,8 +594,21 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
                                                       v_cache, k_scale, v_scale)
     code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
-    dev = _placed("lsa_window_attention", _LSA_WINDOW_ATTENTION, (q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale,
-                  out, lse_out, workspace), 1)
+    dev = q.get_device()
+    if not (dev >= 0
+            and q_offsets.get_device() == dev and q_offsets.is_contiguous()
+            and cache_len.get_device() == dev and cache_len.is_contiguous()
+            and page_table.get_device() == dev and page_table.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and out.get_device() == dev and out.is_contiguous()
+            and workspace.get_device() == dev and workspace.is_contiguous()
+            and (k_scale is None or k_scale.get_device() == dev and k_scale.is_contiguous())
+            and (v_scale is None or v_scale.get_device() == dev and v_scale.is_contiguous())
+            and (lse_out is None or lse_out.get_device() == dev and lse_out.is_contiguous())):
+        _placed("lsa_window_attention", _LSA_WINDOW_ATTENTION,
+                (q, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_scale, out, lse_out,
+                 workspace), 1)
     _on(dev, stream, _lib.lsa_window_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), ccode,
         _ptr(k_scale), _ptr(v_scale), window, n_sink, D ** -0.5 if softmax_scale is None else softmax_scale,
@@ -630,8 +654,25 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
             win_kv = None
         elif win_kv.numel() * win_kv.element_size() < B * W * row_bytes:
             _cap_bytes(B * W * row_bytes, win_kv=win_kv)
-    dev = _placed("lsa_core_attention", _LSA_CORE_ATTENTION, (q, q_offsets, cache_len, page_table, k_cache, v_cache, topk_idx, idx,
-                  count, seq_offsets, hot_kv, win_kv, out, lse_out, workspace), 1)
+    dev = q.get_device()
+    if not (dev >= 0
+            and q_offsets.get_device() == dev and q_offsets.is_contiguous()
+            and cache_len.get_device() == dev and cache_len.is_contiguous()
+            and page_table.get_device() == dev and page_table.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and topk_idx.get_device() == dev and topk_idx.is_contiguous()
+            and idx.get_device() == dev and idx.is_contiguous()
+            and count.get_device() == dev and count.is_contiguous()
+            and seq_offsets.get_device() == dev and seq_offsets.is_contiguous()
+            and hot_kv.get_device() == dev and hot_kv.is_contiguous()
+            and out.get_device() == dev and out.is_contiguous()
+            and workspace.get_device() == dev and workspace.is_contiguous()
+            and (win_kv is None or win_kv.get_device() == dev and win_kv.is_contiguous())
+            and (lse_out is None or lse_out.get_device() == dev and lse_out.is_contiguous())):
+        _placed("lsa_core_attention", _LSA_CORE_ATTENTION,
+                (q, q_offsets, cache_len, page_table, k_cache, v_cache, topk_idx, idx, count, seq_offsets,
+                 hot_kv, win_kv, out, lse_out, workspace), 1)
     _on(dev, stream, _lib.lsa_core_attention, q.data_ptr(), sq, code, q_offsets.data_ptr(), N, B, cache_len.data_ptr(),
         page_table.data_ptr(), max_pages, Hq, H, D, page, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), window, n_sink,
         D ** -0.5 if softmax_scale is None else softmax_scale, topk_idx.data_ptr(), k, idx.data_ptr(), count.data_ptr(),
