@@ -126,6 +126,7 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
         float ks = 1.f, vs = 1.f;
         bool there = false;
         if (t < total) there = cached_rows<CT>(A, b, h, t < sp.sinks ? t : sp.lo + (t - sp.sinks), kr, vr, ks, vs);
+        if (!there) vr = nullptr;  // (a bad scale, NaN among them, must not meet its weight of zero)
         float s = -INFINITY;
         if (there) {
             float d = 0.f;

@@ -1,0 +1,42 @@
+"""Core attention where a kernel leaves its common path: rows that are done again key by key, scales at the ends of
+their range, infinities that a query may see, lengths behind the page table.  Against the definition in 64 bits, on
+both kernels (LSA_ATTN_MANY) where both can take the call."""
+import math
+
+import pytest
+import torch
+
+import attn_oracle as ao
+from test_gpu_attention import BF16, F32, Case, call, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_kv_cache_memoryindexer_b200 as mod
+    mod.lsa_check_device()
+    return mod
+
+
+@pytest.fixture(params=["0", "1"], ids=["few", "many"])
+def kernel(request, monkeypatch):
+    monkeypatch.setenv("LSA_ATTN_MANY", request.param)
+
+
+@pytest.mark.parametrize("n", [9, 60])
+def test_bad_scale_on_rows_that_are_done_again(m, kernel, n):
+    """A token of NaN behind the first rows sends them through the key-by-key way; a page with a NaN scale is left out
+    there too."""
+    from sparse_kv_cache_memoryindexer_b200 import LSAError
+    c = Case([n], [100], 2, 8, 64, 16, BF16, ao.E4M3)
+    d = c.cuda()
+    pg, last = int(c.table[0, 2]), 100 + n - 1
+    d["v_scale"][pg] = math.nan
+    d["v_cache"].view(torch.uint8)[int(c.table[0, last // 16]), :, last % 16] = 0x7F
+    call(m, c, d)
+    with pytest.raises(LSAError, match="scale"):
+        m.lsa_check_device()
+    check(c, d, rows={(0, i) for i in range(n - 1)}, hidden=lambda b, j: j // 16 == 2)
