@@ -274,7 +274,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
     const int G = A.Hq / A.H;
     if (nb == 0) {  // no keys here
         if (part) {
-            for (int r = tid; r < CTA_ROWS; r += C::THREADS) part[r] = -INFINITY;
+            for (int r = tid; r < CTA_ROWS; r += C::THREADS) {
+                part[r] = -INFINITY;
+                part[CTA_ROWS + r] = 0.f;
+            }
         } else {
             for (int i = tid; i < j.rows * (D / 8); i += C::THREADS) {
                 int64_t n, pos;
@@ -843,10 +846,11 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
     for (int e = 0; e < PER; e++) acc[e] = 0.f;
     for (int z = 0; z < Z; z++) {
         const float *p = p0 + z * PF;
-        const float m = p[r];
-        if (m == -INFINITY) continue;  // (a part without keys has written nothing else)
+        const float m = p[r], l = p[CTA_ROWS + r];
+        // a part without keys has written nothing else; one whose scores are all NaN has no maximum either, and a sum of NaN
+        if (m == -INFINITY && l == 0.f) continue;
         const float f = few::exp2_fast(m - M);
-        L = fmaf(p[CTA_ROWS + r], f, L);
+        L = fmaf(l, f, L);
 #pragma unroll
         for (int e = 0; e < PER; e++) acc[e] = fmaf(p[2 * CTA_ROWS + (size_t)r * D + lane + 32 * e], f, acc[e]);
     }

@@ -40,3 +40,20 @@ def test_bad_scale_on_rows_that_are_done_again(m, kernel, n):
     with pytest.raises(LSAError, match="scale"):
         m.lsa_check_device()
     check(c, d, rows={(0, i) for i in range(n - 1)}, hidden=lambda b, j: j // 16 == 2)
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+@pytest.mark.parametrize("old", [40, 9000])
+def test_a_query_of_nan_gives_nan(m, kernel, cdt, old):
+    """With its keys in one part or split over many; the rows beside it are as ever."""
+    c = Case([3, 20], [old, 5], 2, 8, 64, 64, BF16, cdt)
+    d = c.cuda()
+    d["q"][1, 5] = math.nan
+    d["q"][9] = math.nan
+    call(m, c, d)
+    m.lsa_check_device()
+    for n, heads in ((1, [5]), (9, range(8))):
+        for h in heads:
+            assert torch.isnan(d["out"][n, h]).all() and torch.isnan(d["lse_out"][n, h]), (n, h)
+    check(c, d, rows={(0, 0), (0, 2), (1, 0), (1, 5), (1, 7), (1, 19)})
+    assert not torch.isnan(d["out"][1, :5]).any() and not torch.isnan(d["out"][1, 6:]).any()
