@@ -638,9 +638,10 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         if (i >= count) return -1;
         const int u = chunk_of(i);
         if (CORE && u >= s.chunks) return entries[(u - c0) * KEYS + (lane & 15)];
-        // (lanes 0-15 for the first half, the others for the second; its page may lie behind the table's end, unseen)
+        // (lanes 0-15 for the first half, the others for the second; its page may lie behind the table's end: there is none)
         const int at = (pos_of(u) + (KH > 1 ? lane & 16 : 0)) >> A.page_shift;
-        return __ldg(A.page_table + (int64_t)b * A.max_pages + (KH > 1 ? min(at, A.max_pages - 1) : at));
+        if (KH > 1 && at >= A.max_pages) return -1;
+        return __ldg(A.page_table + (int64_t)b * A.max_pages + at);
     };
     // start the loads of the CTA's i-th chunk (warp w takes w, w + WARPS, ..)
     auto issue = [&](int i, int stage, int32_t found) {

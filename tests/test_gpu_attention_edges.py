@@ -57,3 +57,35 @@ def test_a_query_of_nan_gives_nan(m, kernel, cdt, old):
             assert torch.isnan(d["out"][n, h]).all() and torch.isnan(d["lse_out"][n, h]), (n, h)
     check(c, d, rows={(0, 0), (0, 2), (1, 0), (1, 5), (1, 7), (1, 19)})
     assert not torch.isnan(d["out"][1, :5]).any() and not torch.isnan(d["out"][1, 6:]).any()
+
+
+@pytest.mark.parametrize("cdt", [BF16, F32, ao.E4M3])
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_length_behind_an_odd_number_of_pages(m, kernel, cdt, n):
+    """A length that takes the tokens past the page table's end (an odd number of 16-key pages): flagged, and the rows see
+    what the table holds, once."""
+    from sparse_kv_cache_memoryindexer_b200 import LSAError
+    c = Case([n], [112 - n], 2, 8, 64, 16, F32 if cdt == F32 else BF16, cdt)
+    assert c.max_pages == 7
+    d = c.cuda()
+    d["cache_len"][0] = 115
+    call(m, c, d)
+    with pytest.raises(LSAError, match="count"):
+        m.lsa_check_device()
+    for i in range(n):  # (every row stands behind position 111)
+        check_row(c, d, i, range(112))
+
+
+def check_row(c, d, i, keys):
+    """Row i of a case of one sequence, which sees `keys`."""
+    j = torch.tensor(list(keys))
+    pg, sl = c.table[0].long()[j // c.page], j % c.page
+    for hq in range(c.Hq):
+        h = hq // (c.Hq // c.H)
+        K, V = c.kc[pg, :, sl][:, h].double(), c.vc[pg, :, sl][:, h].double()
+        if c.ks is not None:
+            K, V = K * c.ks[pg, h].double()[:, None], V * c.vs[pg, h].double()[:, None]
+        o, l_, A, mag = ao.attend(c.q[i, hq].double(), K, V, c.scale)
+        bo, bl = ao.attend_bounds(o, A, mag, j.numel(), c.D, c.dt, {BF16: BF16, F32: None, ao.E4M3: torch.float16}[c.cdt])
+        assert ((d["out"][i, hq].cpu().double() - o).abs() <= bo).all(), (i, hq)
+        assert abs(float(d["lse_out"][i, hq]) - l_) <= bl, (i, hq)
