@@ -383,7 +383,9 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
  *     lse = log sum_j exp(x_j);   a query that sees no key gets out = 0, lse = -inf.
  *   q            [N][H_q][D] dt, q_stride elements from one token to the next
  *   dt, cdt      LSA_F32 with an LSA_F32 cache; LSA_BF16 with LSA_BF16 or LSA_FP8_E4M3 (k_scale,
- *                v_scale [n_pages][H_kv]: 0, or in [2^-100, 2^120])
+ *                v_scale [n_pages][H_kv]: 0, or in [2^-100, 2^120]; rows that see a value scale outside
+ *                [2^-64, 2^40], or whose largest score is that of a key with a value scale of 0, are
+ *                computed key by key, which is right but slow)
  *   page_table   pages that no query sees are not looked at (they may have been given back)
  *   out          [N][H_q][D] dt; lse_out [N][H_q] fp32 (nullable)
  * Products and sums are fp32; probabilities enter the value product in bf16 (f16 for E4M3 caches).

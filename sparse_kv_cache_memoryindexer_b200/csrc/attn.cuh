@@ -71,9 +71,19 @@ __host__ __device__ __forceinline__ Span visible_span(int64_t p, int window, int
     return s;
 }
 
-// A page scale must be finite, >= 0; a value scale's reciprocal and its product with a long sum are formed
-// in fp32, so one that is not zero lies in [2^-100, 2^120].
+// A page scale: zero, or in [2^-100, 2^120] (finite with room for a code's 448).
 __device__ __forceinline__ bool good_scale(float s) { return s == 0.f || (s >= 7.8886090522101181e-31f && s <= 1.329227995784916e36f); }
+
+// Value scales that the kernels' one reference serves.  A key's weight in the value product is p vs, in the softmax sum p;
+// the kernels hold p' = 2^(s + log2 vs - m'), m' the running maximum of s + log2 vs, and add p' / vs to the sum.  With
+// scales in [2^-64, 2^40] a key that counts in the sum has a p' above fp32's least normal (104 binades apart, and the
+// factor 2^15 or 2^7 of p' leaves it 37 or 29 more), and 2^31 of the largest p' / vs (2^79) stay below 2^128.  What lies
+// outside is rare, and rows that it touches are done again by attend_row, which keeps the two maxima apart:
+//   - a scale outside (values beyond 2^48 or whose largest is below 2^-55): every row of the tile that met it;
+//   - a scale of zero counts as 2^-64 in the sum and as nothing in the value product, which is right unless its keys set m'
+//     (then the others' p' may have vanished): the rows whose maximum is such a key's.
+__device__ __forceinline__ bool odd_value_scale(float s) { return s != 0.f && (s < 5.421010862427522e-20f || s > 1.099511627776e12f); }
+constexpr float ZERO_LV = -64.f, ZERO_INV = 18446744073709551616.f;  // log2 and reciprocal that a scale of zero counts with
 
 // Key and value rows of one cached token of head h, with their page's scales (false: the page is bad, flagged).
 template <int CT>
@@ -101,10 +111,19 @@ __device__ __forceinline__ bool cached_rows(const AttnArgs &A, int b, int h, int
 
 constexpr int ATTN_MAX_D = 128;
 
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
 // One query row (token n, head hq) by one warp, key by key in fp32: 32 keys at a time, a key per lane for the
 // scores, D / 32 dimensions per lane for the values.  The way out for rows whose tile met an infinity or NaN: a
 // matrix product carries one from a key that a row must not see into that row as 0 x inf.  Such a row comes out
-// as NaN, so a row that is not finite is done again here, over its own keys alone.
+// as NaN, so a row that is not finite is done again here, over its own keys alone.  So are rows of E4M3 caches that met
+// unusual value scales (odd_value_scale): the softmax sum is relative to the largest score (m), the value product to the
+// largest score + log2 vs (mo), whatever the scales.
 // qs: the warp's D floats of shared memory.
 template <int QT, int CT>
 __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
@@ -116,7 +135,8 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
     const Span sp = visible_span(pos, A.window, A.n_sink);
     // (a position behind the page table's end, from a bad length, has no keys: the search does not go there)
     const int64_t total = sp.sinks + max((int64_t)0, min(pos + 1, (int64_t)A.max_pages * A.page) - sp.lo);
-    float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
+    const float sl2 = A.scale * 1.4426950408889634f;  // scores in log2 units
+    float m = -INFINITY, l = 0.f, mo = -INFINITY, acc[ATTN_MAX_D / 32];
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;
 #pragma unroll 1
@@ -126,42 +146,48 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
         float ks = 1.f, vs = 1.f;
         bool there = false;
         if (t < total) there = cached_rows<CT>(A, b, h, t < sp.sinks ? t : sp.lo + (t - sp.sinks), kr, vr, ks, vs);
-        if (!there) vr = nullptr;  // (a bad scale, NaN among them, must not meet its weight of zero)
+        if (!there || vs == 0.f) vr = nullptr;  // (a bad scale, NaN among them, must not meet its weight of zero)
         float s = -INFINITY;
         if (there) {
             float d = 0.f;
 #pragma unroll 4
             for (int i = 0; i < D; i++) d += qs[i] * load_elem<CT>(kr, i);
-            s = d * (A.scale * ks);
+            s = d * (sl2 * ks);
         }
-        float mx = s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = __expf(m - ref);
-        const float p = there ? __expf(s - ref) : 0.f;
+        const float mx = warp_max(s), mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+        const float p = there ? exp2f(s - ref) : 0.f;
+        const float f = exp2f(m - ref);
         l = l * f + p;
         m = mn;
+        float w = p, fo = f;  // weight in the value product, and what brings that to its new maximum
+        if constexpr (CT == DT_FP8) {
+            const float y = vr ? s + log2f(vs) : -INFINITY, on = fmaxf(mo, warp_max(y)), oref = on == -INFINITY ? 0.f : on;
+            w = vr ? exp2f(y - oref) : 0.f;
+            fo = exp2f(mo - oref);
+            mo = on;
+        }
 #pragma unroll
-        for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= f;
+        for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= fo;
         const int many = (int)min((int64_t)32, total - t0);
 #pragma unroll 1
         for (int j = 0; j < many; j++) {
-            const float pj = __shfl_sync(0xffffffffu, p * vs, j);
+            const float wj = __shfl_sync(0xffffffffu, w, j);
             const uint8_t *rj = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)vr, j);
             if (!rj) continue;
 #pragma unroll
             for (int i = 0; i < ATTN_MAX_D / 32; i++)
-                if (i < per) acc[i] += pj * load_elem<CT>(rj, lane + 32 * i);
+                if (i < per) acc[i] += wj * load_elem<CT>(rj, lane + 32 * i);
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
+    // (no key with a value: the sums of values are zero, whatever the maxima)
+    const float back = CT == DT_FP8 ? (mo == -INFINITY ? 1.f : exp2f(mo - m)) : 1.f;
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; i++)
-        if (i < per) store_elem<QT>(A.out, (n * A.Hq + hq) * D + lane + 32 * i, acc[i] * inv);
-    if (A.lse && lane == 0) A.lse[n * A.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
+        if (i < per) store_elem<QT>(A.out, (n * A.Hq + hq) * D + lane + 32 * i, acc[i] * inv * back);
+    if (A.lse && lane == 0) A.lse[n * A.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     __syncwarp();
 }
 

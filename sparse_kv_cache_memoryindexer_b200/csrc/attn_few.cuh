@@ -12,9 +12,9 @@
 //   E4M3 cache:  codes decoded exactly to f16; the query row is brought to f16 by a power of two of its
 //                own (elements 2^33 times smaller than the row's largest lose bits, no others).  A page's
 //                value scale vs enters the exponent: p' = 2^(s + log2 vs - m'), with m' the running maximum
-//                of s + log2 vs, so p' is rounded to f16 relative to what it adds to the output whatever the
-//                scales; the softmax sum takes p' / vs in fp32.  p' is kept 2^15 times larger (below f16's
-//                largest), so that only weights under 2^-29 of the largest are subnormal and lose bits.
+//                of s + log2 vs, so p' is rounded to f16 relative to what it adds to the output; the softmax sum
+//                takes p' / vs in fp32 (unusual scales: see odd_value_scale).  p' is kept 2^15 times larger (below
+//                f16's largest), so that only weights under 2^-29 of the largest are subnormal and lose bits.
 //   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
 //                (the fourth, lo lo, is below 2^-22 of the product).
 //
@@ -55,7 +55,8 @@ struct Cfg {
     static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
     static constexpr int NT = D / 8;                // n-tiles of the value product
     static constexpr int QREGS = CT == DT_F32 ? D / 2 : D / 4;  // query fragment registers
-    static constexpr int SMEM = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 32;
+    static constexpr int OFF_ZMAX = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 32;
+    static constexpr int SMEM = OFF_ZMAX + (CT == DT_FP8 ? WARPS * ROWS * 4 : 0);
 };
 
 // 16-byte piece of a row that holds piece c of row `row`: chosen for each access pattern below so that the
@@ -558,9 +559,16 @@ __device__ __forceinline__ void tile_row(const AttnArgs &A, const Seq &s, const 
     }
 }
 
-// A part in the workspace: maxima and sums of 16 rows (of 2^(x - max)), then the sums of values.
+// A part in the workspace: maxima and sums of 16 rows (of 2^(x - max)), then the sums of values.  E4M3: a sum is negative
+// where the maximum is that of a key with a value scale of zero, NaN where a scale is unusual (odd_value_scale).
 template <int D>
 constexpr size_t part_floats() { return 2 * ROWS + (size_t)ROWS * D; }
+
+template <int CT>
+__device__ __forceinline__ float sum_of(float l) { return CT == DT_FP8 ? fabsf(l) : l; }
+// The part (m, l) sets the maximum M, with a key whose value scale is zero.
+template <int CT>
+__device__ __forceinline__ bool from_zero(float l, float m, float M) { return CT == DT_FP8 && l < 0.f && m == M; }
 
 // Chunks [u0, u1) of tile `tile` and head h of sequence b, by the whole CTA.  part: where to leave the sums (null:
 // the outputs are written; with CLUSTER, together with the cluster's other CTAs, which have the tile's other chunks).
@@ -577,6 +585,12 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     struct Meta { float sc[2][2]; uint32_t live, pad[3]; };  // key and value scale of each half; which keys are there
     Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
     const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
+    // E4M3: each row's largest score of a key with a value scale of zero (with its ZERO_LV); infinite: an unusual scale
+    float *zmax = (float *)(smem + C::OFF_ZMAX) + warp * ROWS;
+    if constexpr (CT == DT_FP8) {
+        if (lane < ROWS) zmax[lane] = -INFINITY;
+        __syncwarp();
+    }
 
     int32_t *entries = (int32_t *)(smem + C::SMEM);  // CORE: rows of the part's Top-k entries
 
@@ -744,8 +758,12 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 }
                 if (vs != last_vs[hf]) {
                     last_vs[hf] = vs;
-                    lv[hf] = vs > 0.f ? log2f(vs) : 0.f;
-                    inv_vs[hf] = vs > 0.f ? 1.f / vs : 1.f;
+                    lv[hf] = vs > 0.f ? log2f(vs) : ZERO_LV;
+                    inv_vs[hf] = vs > 0.f ? 1.f / vs : ZERO_INV;
+                    if (good_scale(vs) && odd_value_scale(vs)) {
+                        if (lane < ROWS) zmax[lane] = INFINITY;
+                        __syncwarp();
+                    }
                 }
             }
         }
@@ -775,6 +793,24 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                                      (listed || (pos <= me && (A.window == 0 || pos > me - A.window || pos < A.n_sink)));
                     if (!see) x[j][e] = -INFINITY;
                 }
+        }
+        if constexpr (CT == DT_FP8) {
+            bool zero = false;
+#pragma unroll
+            for (int hf = 0; hf < KH; hf++) zero |= (live >> (16 * hf) & 1) && last_vs[hf] == 0.f;
+            if (zero) {
+#pragma unroll
+                for (int i2 = 0; i2 < 2; i2++) {
+                    float zm = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 2 * KH; j++)
+                        if (last_vs[j / 2] == 0.f) zm = fmaxf(zm, fmaxf(x[j][2 * i2], x[j][2 * i2 + 1]));
+                    zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
+                    zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 2));
+                    if (c == 0) zmax[r + 8 * i2] = fmaxf(zmax[r + 8 * i2], zm);
+                }
+                __syncwarp();
+            }
         }
         bool moved = false;
         float f[2];
@@ -829,6 +865,11 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         if (c == 0) {
+            if constexpr (CT == DT_FP8) {
+                const float zm = zmax[r + 8 * i];
+                if (zm == INFINITY) l[i] = NAN;
+                else if (zm == m[i] && zm != -INFINITY) l[i] = -l[i];
+            }
             ml[warp * ROWS + r + 8 * i] = m[i];
             ml[(WARPS + warp) * ROWS + r + 8 * i] = l[i];
         }
@@ -849,13 +890,14 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     __syncthreads();
     constexpr int GROUPS = D / 4;  // four dimensions of a row each
     uint32_t bad = 0;              // rows of this thread's that are not finite
-    auto write = [&](int row, int d, float4 o, float M, float L) {
+    // (again: the row's maximum is that of a key with a value scale of zero)
+    auto write = [&](int row, int d, float4 o, float M, float L, bool again) {
         int n, pos, g;
         tile_row<CORE>(A, s, t, row, n, pos, g);
         const int64_t at = (int64_t)n * A.Hq + h * G + g;
         const float inv = L == 0.f ? 0.f : 1.f / L;
         o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        if (!finite4(o)) bad |= 1u << row;
+        if (again || !finite4(o)) bad |= 1u << row;
         if constexpr (QT == DT_F32)
             *(float4 *)((float *)A.out + at * D + d) = o;
         else
@@ -870,13 +912,15 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         const int row = i / GROUPS, d = (i % GROUPS) * 4;
         if (row >= t.rows) continue;
         float M = ml[row], L = 0.f;
+        bool zero = false;
 #pragma unroll
         for (int w = 1; w < WARPS; w++) M = fmaxf(M, ml[w * ROWS + row]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WARPS; w++) {
-            const float mw = ml[w * ROWS + row];
-            L += ml[(WARPS + w) * ROWS + row] * (mw == -INFINITY ? 0.f : exp2_fast(mw - M));
+            const float mw = ml[w * ROWS + row], lw = ml[(WARPS + w) * ROWS + row];
+            L += sum_of<CT>(lw) * (mw == -INFINITY ? 0.f : exp2_fast(mw - M));
+            zero |= from_zero<CT>(lw, mw, M);
             const float4 v = *(const float4 *)((const float *)smem + (w * ROWS + row) * D + d);
             o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
         }
@@ -884,11 +928,11 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             float *to = part ? part : own;
             if (d == 0) {
                 to[row] = M;
-                to[ROWS + row] = L;
+                to[ROWS + row] = zero ? -L : L;
             }
             *(float4 *)(to + 2 * ROWS + row * D + d) = o;
         } else {
-            write(row, d, o, M, L);
+            write(row, d, o, M, L, zero);
         }
     }
     if (CLUSTER && ranks > 1) {
@@ -898,22 +942,26 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             const int row = (int)(me * per) + i / GROUPS, d = (i % GROUPS) * 4;
             if (row >= t.rows) continue;
             float M = -INFINITY, L = 0.f;
+            bool zero = false;
             for (uint32_t w = 0; w < ranks; w++) M = fmaxf(M, ld_cluster(own_a + row * 4, w));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (uint32_t w = 0; w < ranks; w++) {
                 const float mw = ld_cluster(own_a + row * 4, w), f = mw == -INFINITY ? 0.f : exp2_fast(mw - M);
                 const float4 v = ld_cluster4(own_a + (2 * ROWS + row * D + d) * 4, w);
-                L = fmaf(ld_cluster(own_a + (ROWS + row) * 4, w), f, L);
+                const float lw = ld_cluster(own_a + (ROWS + row) * 4, w);
+                L = fmaf(sum_of<CT>(lw), f, L);
+                zero |= from_zero<CT>(lw, mw, M);
                 o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
             }
-            write(row, d, o, M, L);
+            write(row, d, o, M, L, zero);
         }
         cluster_sync();  // (nobody leaves, or writes its ring, while the others read its sums)
     }
     __syncthreads();  // the ring is free again
     if constexpr (!CORE) {
-        // rows of several tokens: one that is not finite may have met another's key (see attend_row)
-        if (!part && t.p_lo != t.p_hi) {
+        // rows of several tokens: one that is not finite may have met another's key; and rows with unusual value scales
+        // (see attend_row)
+        if (!part && (t.p_lo != t.p_hi || CT == DT_FP8)) {
             bad = __reduce_or_sync(0xffffffffu, bad);
             uint32_t *rows = (uint32_t *)smem;
             if (lane == 0) rows[warp] = bad;
@@ -1107,13 +1155,15 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     constexpr int PER = D / 32;
     float acc[PER], L = 0.f;
+    bool zero = false;
 #pragma unroll
     for (int e = 0; e < PER; e++) acc[e] = 0.f;
 #pragma unroll 4
     for (int i = c0; i <= c1; i++) {
         const float *p = part(i);
         const float m = p[row], f = m == -INFINITY ? 0.f : exp2_fast(m - M);
-        L = fmaf(p[ROWS + row], f, L);
+        L = fmaf(sum_of<CT>(p[ROWS + row]), f, L);
+        zero |= from_zero<CT>(p[ROWS + row], m, M);
 #pragma unroll
         for (int e = 0; e < PER; e++) acc[e] = fmaf(p[2 * ROWS + row * D + lane + 32 * e], f, acc[e]);
     }
@@ -1121,7 +1171,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     tile_row<CORE>(A, s, t, row, n, pos, g);
     const int64_t at = (int64_t)n * A.Hq + h * G + g;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    bool bad = false;
+    bool bad = zero;
 #pragma unroll
     for (int e = 0; e < PER; e++) {
         const float v = acc[e] * inv;
@@ -1131,7 +1181,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
     if (A.lse && lane == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - shift + log2f(L)) * 0.6931471805599453f;
     if constexpr (!CORE) {
         __shared__ float qs[JOIN_ROWS][ATTN_MAX_D];
-        if (t.p_lo != t.p_hi && __any_sync(0xffffffffu, bad)) attend_row<QT, CT>(A, b, pos, n, h * G + g, qs[threadIdx.x >> 5]);
+        if ((t.p_lo != t.p_hi || CT == DT_FP8) && __any_sync(0xffffffffu, bad)) attend_row<QT, CT>(A, b, pos, n, h * G + g, qs[threadIdx.x >> 5]);
     }
 }
 

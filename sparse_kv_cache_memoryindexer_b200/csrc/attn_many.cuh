@@ -69,7 +69,7 @@ struct Cfg {
 constexpr float STALE = 8.f;  // log2 of how far a row's maximum may run ahead of the one in use
 
 // Page data of a block: for each 16 keys the key scale, log2 of the value scale and its reciprocal; which are live,
-// and which have a value scale of zero.
+// and which have a value scale of zero (bit 8: some page has an unusual one, see odd_value_scale).
 struct Meta {
     float ks[8], lv[8], inv[8];
     uint32_t live, zero, pad[2];
@@ -190,7 +190,8 @@ __device__ __forceinline__ void row_of(const AttnArgs &A, const Job &j, int r, i
     g = R % G;
 }
 
-// A part in the workspace: maxima (log2, of what the exponents are relative to) and sums of 256 rows, then O.
+// A part in the workspace: maxima (log2, of what the exponents are relative to) and sums of 256 rows, then O.  E4M3: a
+// sum is negative where the maximum is that of a key with a value scale of zero, NaN where a scale is unusual.
 template <int D>
 constexpr size_t part_floats() { return 2 * CTA_ROWS + (size_t)CTA_ROWS * D; }
 
@@ -398,6 +399,9 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         // (a factor of zero would make NaN of a masked -inf)
         const float f = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1e-30f) * (FP8 ? qfac[r] : 1.f);
         const float fx = FP8 ? 1.f : f;  // from s to log2 units
+        // E4M3: the last maximum that a key with a value scale of zero has set; infinite: an unusual scale was met.  (In
+        // the row factor's place, which nobody else reads: a register less through the loop.)
+        if (FP8) qfac[r] = -INFINITY;
         float m = -INFINITY, l = 0.f;    // m: the maximum in use, in the units of s
         bool ok = true;
         for (int i = 0; i < nb; i++) {
@@ -440,15 +444,16 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     for (int k = 0; k < 32; k++) s[pc][k] = (w & (1u << k)) ? s[pc][k] : -INFINITY;
                 }
             }
-            float mx4[4];
+            float mx8[8];  // (of each 16 keys)
 #pragma unroll
-            for (int pc = 0; pc < 4; pc++) {
-                mx4[pc] = s[pc][0];
+            for (int k8 = 0; k8 < 8; k8++) {
+                const float *x16 = &s[k8 / 2][16 * (k8 & 1)];
+                mx8[k8] = x16[0];
 #pragma unroll
-                for (int k = 1; k < 31; k += 2) mx4[pc] = fmaxf(fmaxf(mx4[pc], s[pc][k]), s[pc][k + 1]);
-                mx4[pc] = fmaxf(mx4[pc], s[pc][31]);
+                for (int k = 1; k < 15; k += 2) mx8[k8] = fmaxf(fmaxf(mx8[k8], x16[k]), x16[k + 1]);
+                mx8[k8] = fmaxf(mx8[k8], x16[15]);
             }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
             const bool grow = m == -INFINITY ? mx != -INFINITY : (mx - m) * fx > STALE;
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = fmaxf(m, mx);
@@ -469,6 +474,13 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     }
                     tmem_wait_st();
                 }
+            }
+            if (FP8 && me->zero) {
+                float zm = -INFINITY;
+#pragma unroll
+                for (int k8 = 0; k8 < 8; k8++) zm = fmaxf(zm, (me->zero >> k8 & 1) ? mx8[k8] : -INFINITY);
+                if (me->zero >> 8) qfac[r] = INFINITY;
+                else if (zm == m && qfac[r] != INFINITY) qfac[r] = m;
             }
             const float ref = (m == -INFINITY ? 0.f : m) * fx - C::SHIFT;
             float2 sum = make_float2(0.f, 0.f);
@@ -503,10 +515,15 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         if (ok && !wait_warp(o_done(t), (nb - 1) & 1, abort_flag)) ok = false;
         if (ok) {
             tc_fence_after();
+            bool bad = false;
+            if constexpr (FP8) {
+                if (qfac[r] == INFINITY) l = NAN;
+                else bad = qfac[r] == m && m != -INFINITY && r < j.rows;
+            }
+            const bool zero = bad;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float ml2 = m * (FP8 ? 1.f : f) - C::SHIFT;
             const int64_t at = n * A.Hq + h * G + g;
-            bool bad = false;
 #pragma unroll
             for (int pc = 0; pc < D / 32; pc++) {
                 float v[32];
@@ -535,12 +552,12 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             if (r < j.rows) {
                 if (part) {
                     part[r] = m == -INFINITY ? -INFINITY : ml2;
-                    part[CTA_ROWS + r] = l;
+                    part[CTA_ROWS + r] = zero ? -l : l;
                 } else if (A.lse) {
                     A.lse[at] = l == 0.f ? -INFINITY : (ml2 + log2f(l)) * 0.6931471805599453f;
                 }
             }
-            uint32_t again = __ballot_sync(0xffffffffu, bad);
+            uint32_t again = part ? 0u : __ballot_sync(0xffffffffu, bad);
             while (again) {  // (this tile's products are done: its query tile is free for the rows)
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
@@ -596,7 +613,8 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 if (!wait_warp(FP8 ? kraw_empty : k_empty(i & 1), FP8 ? (i & 1) ^ 1 : ((i >> 1) & 1) ^ 1, abort_flag)) break;
                 Meta *me = meta + (i & (META - 1));
                 if (lane < per_block) {
-                    const float lv = FP8 && page >= 0 && vs > 0.f ? log2f(vs) : 0.f, inv = FP8 && page >= 0 && vs > 0.f ? 1.f / vs : 1.f;
+                    const float lv = !FP8 ? 0.f : (page >= 0 && vs > 0.f ? log2f(vs) : ZERO_LV);
+                    const float inv = !FP8 ? 1.f : (page >= 0 && vs > 0.f ? 1.f / vs : ZERO_INV);
                     for (int k = 0; k < A.page / 16; k++) {
                         const int at = lane * (A.page / 16) + k;
                         me->ks[at] = page >= 0 ? ks : 0.f;
@@ -607,6 +625,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                 uint32_t live = 0, zero = 0;
                 {
                     const uint32_t zs = __ballot_sync(0xffffffffu, page >= 0 && vs == 0.f);
+                    if (__any_sync(0xffffffffu, FP8 && page >= 0 && odd_value_scale(vs))) zero = 256u;
                     for (int k = 0; k < 8; k++) {
                         const int p = k * 16 / A.page;
                         live |= (there >> p & 1u) << k;
@@ -842,6 +861,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
     for (int z = 0; z < Z; z++) M = fmaxf(M, p0[z * PF + r]);
     constexpr int PER = D / 32;
     float acc[PER], L = 0.f;
+    bool zero = false;
 #pragma unroll
     for (int e = 0; e < PER; e++) acc[e] = 0.f;
     for (int z = 0; z < Z; z++) {
@@ -850,7 +870,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
         // a part without keys has written nothing else; one whose scores are all NaN has no maximum either, and a sum of NaN
         if (m == -INFINITY && l == 0.f) continue;
         const float f = few::exp2_fast(m - M);
-        L = fmaf(l, f, L);
+        L = fmaf(few::sum_of<CT>(l), f, L);
+        zero |= few::from_zero<CT>(l, m, M);
 #pragma unroll
         for (int e = 0; e < PER; e++) acc[e] = fmaf(p[2 * CTA_ROWS + (size_t)r * D + lane + 32 * e], f, acc[e]);
     }
@@ -860,7 +881,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_many_join(const AttnAr
     row_of(A, j, r, n, pos, g);
     const int64_t at = n * A.Hq + h * G + g;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    bool bad = false;
+    bool bad = zero;
 #pragma unroll
     for (int e = 0; e < PER; e++) {
         const float v = acc[e] * inv;

@@ -89,3 +89,70 @@ def check_row(c, d, i, keys):
         bo, bl = ao.attend_bounds(o, A, mag, j.numel(), c.D, c.dt, {BF16: BF16, F32: None, ao.E4M3: torch.float16}[c.cdt])
         assert ((d["out"][i, hq].cpu().double() - o).abs() <= bo).all(), (i, hq)
         assert abs(float(d["lse_out"][i, hq]) - l_) <= bl, (i, hq)
+
+
+# value scales of pages beside one another
+MIXED = [(0.0, 2.0 ** -20), (0.0, 2.0 ** -40), (0.0, 2.0 ** -100), (0.0, 2.0 ** 100), (2.0 ** -64, 2.0 ** 40),
+         (2.0 ** -64, 2.0 ** 70), (2.0 ** -100, 2.0 ** 118), (2.0 ** -100, 2.0 ** -100), (2.0 ** 118, 2.0 ** 118),
+         (0.0, 2.0 ** -64, 1.0), (0.0, 0.02), (2.0 ** -64, 0.02)]
+
+
+def kind(j, values):
+    """Which of the scales page j has: neighbours differ, and so do pages that are four apart."""
+    return (j // 4 + j) % len(values)
+
+
+def scales(c, values):
+    for j in range(c.max_pages):
+        c.vs[int(c.table[0, j])] = values[kind(j, values)]
+    c.vc = c.vc.float().abs().clamp(min=2.0 ** -6).to(ao.E4M3)  # (so that what a page adds cannot cancel)
+    return c
+
+
+@pytest.mark.parametrize("values", MIXED)
+@pytest.mark.parametrize("n,old", [(1, 300), (1, 6000), (50, 300), (300, 6000)])
+def test_value_scales_far_apart(m, kernel, values, n, old):
+    """Every scale that the call accepts, beside every other, in one part and in many."""
+    c = scales(Case([n], [old], 2, 8, 128, 32, BF16, ao.E4M3), values)
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    check(c, d, rows={(0, i) for i in {0, n // 2, n - 1}})
+
+
+@pytest.mark.parametrize("loud", [8.0, 60.0])
+@pytest.mark.parametrize("values", [(0.0, 0.02), (0.0, 2.0 ** -64), (0.0, 2.0 ** 60), (2.0 ** -64, 2.0 ** 40)])
+@pytest.mark.parametrize("n,old", [(1, 300), (1, 6000), (3, 40), (50, 300), (300, 6000)])
+def test_keys_of_zero_scale_with_the_largest_scores(m, kernel, loud, values, n, old):
+    """The pages whose values are zero (or least) have the largest scores, by up to hundreds of binades: the others still
+    carry the output."""
+    c = scales(Case([n], [old], 2, 8, 128, 32, BF16, ao.E4M3), values)
+    for j in range(c.max_pages):
+        if kind(j, values) == 0:
+            c.ks[int(c.table[0, j])] *= loud
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    check(c, d, rows={(0, i) for i in {0, n // 2, n - 1}})
+
+
+@pytest.mark.parametrize("value", [2.0 ** -100, 2.0 ** -64, 2.0 ** 120, 0.0])
+def test_least_and_largest_scale_over_many_keys(m, kernel, value):
+    """Tens of thousands of keys of nearly equal weight: the sum does not overflow."""
+    c = scales(Case([2], [40000], 1, 4, 64, 64, BF16, ao.E4M3, spread=0.01), [value])
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    check(c, d)
+
+
+def test_unusual_scales_of_ragged_users(m, kernel):
+    """Only the sequence that holds them is concerned; rows that see none of the pages are as ever."""
+    c = Case([1, 4, 0, 30], [700, 90, 5, 129], 2, 16, 64, 16, BF16, ao.E4M3, window=200, sinks=3, spare_rows=2)
+    c.vs[int(c.table[0, 40])] = 2.0 ** 90
+    c.vs[int(c.table[1, 2])] = 0.0
+    c.vs[int(c.table[3, 3])] = 2.0 ** -90
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    check(c, d)
