@@ -118,14 +118,44 @@ __device__ __forceinline__ float warp_max(float x)
     return x;
 }
 
+// Key and value rows of Top-k entry e of sequence b, head h (false: none, flagged where the entry is nowhere).
+template <int CT>
+__device__ __forceinline__ bool listed_rows(const AttnArgs &A, int b, int h, int32_t e, const uint8_t *&k, const uint8_t *&v)
+{
+    const int64_t off = __ldg(A.seq_offsets + b), S = __ldg(A.seq_offsets + b + 1) - off;
+    if (e < 0 || off < 0 || S < 0 || off + S > A.total_S) return false;
+    const uint8_t *row = nullptr;
+    if (e >= S) {
+        if (e - S < A.W) row = A.win_kv + ((int64_t)b * A.W + (e - S)) * A.row_bytes;
+    } else {
+        const int cnt = __ldg(A.count + b);
+        int at = 0;
+        for (int c = cnt >= 0 && cnt <= S ? cnt : 0; c > 1;) {  // last place of the ascending list whose entry is <= e
+            const int half = c >> 1;
+            at += __ldg(A.idx + off + at + half) <= e ? half : 0;
+            c -= half;
+        }
+        if (cnt > 0 && cnt <= S && __ldg(A.idx + off + at) == e) row = A.hot_kv + (off + at) * A.row_bytes;
+    }
+    if (!row) {
+        flag(ERRF_INDEX);
+        return false;
+    }
+    constexpr int bytes = CT == DT_F32 ? 4 : 2;
+    k = row + (int64_t)h * A.D * bytes;
+    v = k + (int64_t)A.H * A.D * bytes;
+    return true;
+}
+
 // One query row (token n, head hq) by one warp, key by key in fp32: 32 keys at a time, a key per lane for the
 // scores, D / 32 dimensions per lane for the values.  The way out for rows whose tile met an infinity or NaN: a
 // matrix product carries one from a key that a row must not see into that row as 0 x inf.  Such a row comes out
 // as NaN, so a row that is not finite is done again here, over its own keys alone.  So are rows of E4M3 caches that met
 // unusual value scales (odd_value_scale): the softmax sum is relative to the largest score (m), the value product to the
-// largest score + log2 vs (mo), whatever the scales.
+// largest score + log2 vs (mo), whatever the scales.  And fp32 rows that are not finite: the split into two tf32 parts
+// makes NaN of an infinity (and of a number next to fp32's largest) that the row does see (CORE: with its Top-k entries).
 // qs: the warp's D floats of shared memory.
-template <int QT, int CT>
+template <int QT, int CT, bool CORE = false>
 __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos, int64_t n, int hq, float *qs)
 {
     const int lane = threadIdx.x & 31;
@@ -139,13 +169,18 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
     float m = -INFINITY, l = 0.f, mo = -INFINITY, acc[ATTN_MAX_D / 32];
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] = 0.f;
+    // (the cached keys, then the Top-k list's: each from a number of its own that is a multiple of 32)
+    const int64_t cached = (total + 31) & ~(int64_t)31, keys = CORE ? cached + A.k : total;
 #pragma unroll 1
-    for (int64_t t0 = 0; t0 < total; t0 += 32) {
+    for (int64_t t0 = 0; t0 < keys; t0 += 32) {
         const int64_t t = t0 + lane;
         const uint8_t *kr = nullptr, *vr = nullptr;
         float ks = 1.f, vs = 1.f;
         bool there = false;
         if (t < total) there = cached_rows<CT>(A, b, h, t < sp.sinks ? t : sp.lo + (t - sp.sinks), kr, vr, ks, vs);
+        if constexpr (CORE) {
+            if (t >= cached && t < keys) there = listed_rows<CT>(A, b, h, __ldg(A.topk_idx + n * A.k + (t - cached)), kr, vr);
+        }
         if (!there || vs == 0.f) vr = nullptr;  // (a bad scale, NaN among them, must not meet its weight of zero)
         float s = -INFINITY;
         if (there) {
@@ -168,7 +203,7 @@ __device__ __forceinline__ void attend_row(const AttnArgs &A, int b, int64_t pos
         }
 #pragma unroll
         for (int i = 0; i < ATTN_MAX_D / 32; i++) acc[i] *= fo;
-        const int many = (int)min((int64_t)32, total - t0);
+        const int many = (int)min((int64_t)32, keys - t0);
 #pragma unroll 1
         for (int j = 0; j < many; j++) {
             const float wj = __shfl_sync(0xffffffffu, w, j);

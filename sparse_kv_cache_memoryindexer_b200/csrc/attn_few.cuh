@@ -958,10 +958,10 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         cluster_sync();  // (nobody leaves, or writes its ring, while the others read its sums)
     }
     __syncthreads();  // the ring is free again
-    if constexpr (!CORE) {
-        // rows of several tokens: one that is not finite may have met another's key; and rows with unusual value scales
-        // (see attend_row)
-        if (!part && (t.p_lo != t.p_hi || CT == DT_FP8)) {
+    if constexpr (!CORE || CT == DT_F32) {
+        // rows of several tokens: one that is not finite may have met another's key; fp32 rows that are not finite; rows
+        // with unusual value scales (see attend_row)
+        if (!part && (t.p_lo != t.p_hi || CT != DT_BF16)) {
             bad = __reduce_or_sync(0xffffffffu, bad);
             uint32_t *rows = (uint32_t *)smem;
             if (lane == 0) rows[warp] = bad;
@@ -973,7 +973,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 if (!(bad >> row & 1)) continue;
                 int n, pos, g;
                 tile_row<CORE>(A, s, t, row, n, pos, g);
-                attend_row<QT, CT>(A, b, pos, n, h * G + g, (float *)smem + warp * ATTN_MAX_D);
+                attend_row<QT, CT, CORE>(A, b, pos, n, h * G + g, (float *)smem + warp * ATTN_MAX_D);
             }
             __syncthreads();
         }
@@ -1179,9 +1179,10 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
         store_elem<QT>(A.out, at * D + lane + 32 * e, v);
     }
     if (A.lse && lane == 0) A.lse[at] = L == 0.f ? -INFINITY : (M - shift + log2f(L)) * 0.6931471805599453f;
-    if constexpr (!CORE) {
+    if constexpr (!CORE || CT == DT_F32) {
         __shared__ float qs[JOIN_ROWS][ATTN_MAX_D];
-        if ((t.p_lo != t.p_hi || CT == DT_FP8) && __any_sync(0xffffffffu, bad)) attend_row<QT, CT>(A, b, pos, n, h * G + g, qs[threadIdx.x >> 5]);
+        if ((t.p_lo != t.p_hi || CT != DT_BF16) && __any_sync(0xffffffffu, bad))
+            attend_row<QT, CT, CORE>(A, b, pos, n, h * G + g, qs[threadIdx.x >> 5]);
     }
 }
 

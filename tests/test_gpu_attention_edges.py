@@ -156,3 +156,36 @@ def test_unusual_scales_of_ragged_users(m, kernel):
     call(m, c, d)
     m.lsa_check_device()
     check(c, d)
+
+
+@pytest.mark.parametrize("n,old,window", [(1, 40, 0), (1, 5000, 0), (3, 40, 0), (1, 300, 20), (40, 30, 0)])
+@pytest.mark.parametrize("listed", [0, 50])
+def test_infinities_that_an_fp32_row_sees(m, n, old, window, listed):
+    """A key of -inf weighs nothing, a value of infinity makes the output infinite, numbers next to the largest stay
+    finite: as in the formula, for cached keys and listed ones."""
+    c = Case([n], [old], 2, 8, 64, 16, F32, window=window)
+    c.q = c.q.abs() + 0.1
+    at = lambda p: (int(c.table[0, p // 16]), slice(None), p % 16)  # noqa: E731
+    c.kc[at(old)][:, 5] = -math.inf      # (every row sees the first new token, and the one before it)
+    c.vc[at(old - 1)][1, 7] = -3.4028e38
+    if listed:
+        c.add_topk(listed, [300], [100], 4)
+        held, light = c.idx[:100].tolist(), c.topk[0, 3:6].tolist()
+        row_of = lambda e: c.win[0, e - 300] if e >= 300 else c.hot[held.index(e)]  # noqa: E731
+        for e in light:
+            row_of(e)[0, :, 9] = -math.inf
+        row_of(int(c.topk[0, 6]))[1, 0, 11] = 3.4028e38
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    assert torch.isfinite(d["out"]).all() and torch.isfinite(d["lse_out"]).all()
+    if listed:
+        c.topk[torch.isin(c.topk, torch.tensor(light, dtype=torch.int32))] = -1
+    check(c, d, rows={(0, i) for i in {0, n // 2, n - 1}}, hidden=lambda b, j: j == old)
+    c.vc[at(old - 1)][1, 7] = math.inf
+    e = c.cuda()
+    call(m, c, e)
+    m.lsa_check_device()
+    assert (e["out"][:, 4:, 7] == math.inf).all()
+    e["out"][:, 4:, 7] = d["out"][:, 4:, 7]
+    assert torch.equal(e["out"], d["out"]) and torch.equal(e["lse_out"], d["lse_out"])
