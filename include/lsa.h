@@ -395,7 +395,10 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
  * rule on the sizes picks the faster, LSA_ATTN_MANY=0 or 1 in the environment takes the one or the
  * other wherever it can (the same result up to rounding).
  * Workspace: lsa_window_attention_workspace_size (partial results of keys split over CTAs); it needs
- * no initial content.  Calls that may run at the same time (streams, graphs) need one each.
+ * no initial content.  The size is not monotone in N: a few tokens' keys are split furthest.  A workspace
+ * of the size for any N and B (of the same D) serves every call, with its keys split into as many parts as it
+ * holds (the same result up to rounding); the largest of the sizes gives every call its full speed.
+ * Calls that may run at the same time (streams, graphs) need one each.
  * ---------------------------------------------------------------------------------------- */
 size_t lsa_window_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D);
 

@@ -909,15 +909,23 @@ inline int most_splits(int64_t N, int B, int Hq, int H, int sms)
     return (int)std::min<int64_t>(64, std::max<int64_t>(1, 2 * (int64_t)sms / ctas));
 }
 
+// Bytes of one part of every tile and head.
+inline size_t part_bytes(int64_t N, int B, int Hq, int H, int D)
+{
+    return (size_t)tiles_of(N, B, Hq / H) * H * (2 * CTA_ROWS + (size_t)CTA_ROWS * D) * sizeof(float);
+}
+
 // CTAs that share one tile's keys, tiles of `blocks` blocks at most: the number with the least time, counted in blocks:
 // the waves of CTAs, each its share of the blocks and about four for its start and end, and about eight for the second
-// launch.  (128 tiles of 34 blocks: 100 us whole, 140 in two parts, which make two waves.)  least: that time.
-inline int splits_of(int64_t N, int B, int Hq, int H, int sms, int64_t blocks, int64_t *least)
+// launch.  (128 tiles of 34 blocks: 100 us whole, 140 in two parts, which make two waves.)  No more than the workspace has
+// room for, whatever size it was made for (a whole tile needs none).  least: that time.
+inline int splits_of(int64_t N, int B, int Hq, int H, int D, int sms, int64_t blocks, size_t workspace_bytes, int64_t *least)
 {
     const int64_t ctas = likely_ctas(N, B, Hq, H);
+    const int most = (int)std::min<size_t>(most_splits(N, B, Hq, H, sms), workspace_bytes / part_bytes(N, B, Hq, H, D));
     int best = 1;
     *least = INT64_MAX;
-    for (int z = 1; z <= most_splits(N, B, Hq, H, sms); z++) {
+    for (int z = 1; z <= std::max(most, 1); z++) {
         const int64_t t = (ctas * z + sms - 1) / sms * ((blocks + z - 1) / z + 4) + (z > 1 ? 8 : 0);
         if (t < *least) {
             *least = t;
@@ -937,9 +945,9 @@ inline int64_t likely_keys(const AttnArgs &A)
 inline size_t parts_bytes(int64_t N, int B, int Hq, int H, int D)
 {
     if (Hq % H) return 0;
-    const int z = most_splits(N, B, Hq, H, 160);  // (grows with the SMs: enough for any number up to 160)
+    const int z = most_splits(N, B, Hq, H, 160);  // (what 148 SMs can use, and a few more)
     if (z == 1) return 0;
-    return (size_t)tiles_of(N, B, Hq / H) * H * z * (2 * CTA_ROWS + (size_t)CTA_ROWS * D) * sizeof(float);
+    return z * part_bytes(N, B, Hq, H, D);
 }
 
 // Tensor map of a cache as rows of D elements, a box of one page (bf16: half rows of 64, 128-byte swizzle).
@@ -964,7 +972,7 @@ inline bool make_cache_map(CUtensorMap *m, const void *ptr, bool fp8, int64_t ro
 // 138 : 175; 64 rows 315 : 141, 259 : 176.  One user, 8 heads, window 512, 128 rows: 12 : 18, 13 : 24.  One user, one
 // head, 131072 keys: 64 rows 45 : 51, 47 : 61; 128 rows 62 : 52, 68 : 64.  LSA_ATTN_MANY=0 or 1 in the environment takes
 // the one or the other wherever it can (to check them against one another).
-inline bool takes(const AttnArgs &A, int cdt, int sms)
+inline bool takes(const AttnArgs &A, int cdt, size_t workspace_bytes, int sms)
 {
     if (cdt == DT_F32 || A.k > 0 || (A.D != 64 && A.D != 128)) return false;
     if (A.n_pages * A.H * A.page >= (int64_t)1 << 31 || A.H > 65535) return false;
@@ -972,14 +980,14 @@ inline bool takes(const AttnArgs &A, int cdt, int sms)
     if (env && env[0] == '0') return false;
     const int64_t rows = std::max<int64_t>(A.N / A.B, 1) * (A.Hq / A.H), keys = likely_keys(A);
     int64_t blocks;
-    splits_of(A.N, A.B, A.Hq, A.H, sms, keys / BLOCK + 1, &blocks);
+    splits_of(A.N, A.B, A.Hq, A.H, A.D, sms, keys / BLOCK + 1, workspace_bytes, &blocks);
     const double few_us = 8 + (cdt == DT_FP8 ? 1.12 : 1.45) * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
     const double many_us = 5 + (cdt == DT_FP8 ? 2.2 : 1.8) * blocks;
     return ((env && env[0] == '1') || many_us < few_us) && tc_available();
 }
 
 template <int CT, int D>
-cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st, int *launches)
+cudaError_t launch(const AttnArgs &A, void *workspace, size_t workspace_bytes, int sms, cudaStream_t st, int *launches)
 {
     using C = Cfg<CT, D>;
     CUtensorMap km, vm;
@@ -992,7 +1000,7 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
     if (e != cudaSuccess) return e;
     const int64_t tiles = tiles_of(A.N, A.B, A.Hq / A.H);
     int64_t least;
-    const int Z = splits_of(A.N, A.B, A.Hq, A.H, sms, likely_keys(A) / BLOCK + 1, &least);
+    const int Z = splits_of(A.N, A.B, A.Hq, A.H, A.D, sms, likely_keys(A) / BLOCK + 1, workspace_bytes, &least);
     k_attn_many<CT, D><<<dim3((unsigned)tiles, (unsigned)A.H, (unsigned)Z), C::THREADS, C::SMEM, st>>>(A, km, vm, (float *)workspace);
     ++*launches;
     if (Z == 1) return cudaSuccess;

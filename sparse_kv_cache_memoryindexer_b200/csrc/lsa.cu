@@ -1145,11 +1145,11 @@ lsa_status attention(const char *what, AttnArgs &A, int dt, int cdt, void *works
         if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, true>(A, workspace, num_sms(), st, &n);
         else e = few::launch_d<DT_BF16, DT_BF16, true>(A, workspace, num_sms(), st, &n);
     } else {
-        if (many::takes(A, cdt, num_sms())) {
-            if (cdt == DT_BF16) e = A.D == 64 ? many::launch<DT_BF16, 64>(A, workspace, num_sms(), st, &n)
-                                              : many::launch<DT_BF16, 128>(A, workspace, num_sms(), st, &n);
-            else e = A.D == 64 ? many::launch<DT_FP8, 64>(A, workspace, num_sms(), st, &n)
-                               : many::launch<DT_FP8, 128>(A, workspace, num_sms(), st, &n);
+        if (many::takes(A, cdt, workspace_bytes, num_sms())) {
+            if (cdt == DT_BF16) e = A.D == 64 ? many::launch<DT_BF16, 64>(A, workspace, workspace_bytes, num_sms(), st, &n)
+                                              : many::launch<DT_BF16, 128>(A, workspace, workspace_bytes, num_sms(), st, &n);
+            else e = A.D == 64 ? many::launch<DT_FP8, 64>(A, workspace, workspace_bytes, num_sms(), st, &n)
+                               : many::launch<DT_FP8, 128>(A, workspace, workspace_bytes, num_sms(), st, &n);
         } else if (dt == DT_F32) e = few::launch_d<DT_F32, DT_F32, false>(A, workspace, num_sms(), st, &n);
         else if (cdt == DT_BF16) e = few::launch_d<DT_BF16, DT_BF16, false>(A, workspace, num_sms(), st, &n);
         else e = few::launch_d<DT_BF16, DT_FP8, false>(A, workspace, num_sms(), st, &n);
@@ -1225,8 +1225,9 @@ lsa_status lsa_window_attention(const void *q, int64_t q_stride, lsa_dtype dt, c
     A.k_cache = k_cache; A.v_cache = v_cache; A.k_scale = k_scale; A.v_scale = v_scale; A.out = out; A.lse = lse_out;
     A.N = N; A.n_pages = n_pages; A.B = B; A.max_pages = max_pages; A.Hq = H_q; A.H = H_kv; A.D = D;
     A.page = page_size; A.window = window; A.n_sink = n_sink; A.scale = softmax_scale;
-    return attention("lsa_window_attention", A, dt, cdt, workspace, workspace_bytes,
-                     lsa_window_attention_workspace_size(N, B, H_q, H_kv, D), (cudaStream_t)stream);
+    // (a workspace made for any number of tokens serves: the many-row kernel splits into as many parts as it holds)
+    const size_t need = lsa_core_attention_workspace_size(N, B, H_q, H_kv, D, 0);
+    return attention("lsa_window_attention", A, dt, cdt, workspace, workspace_bytes, need, (cudaStream_t)stream);
 }
 
 size_t lsa_core_attention_workspace_size(int64_t N, int B, int H_q, int H_kv, int D, int k)

@@ -189,3 +189,19 @@ def test_infinities_that_an_fp32_row_sees(m, n, old, window, listed):
     assert (e["out"][:, 4:, 7] == math.inf).all()
     e["out"][:, 4:, 7] = d["out"][:, 4:, 7]
     assert torch.equal(e["out"], d["out"]) and torch.equal(e["lse_out"], d["lse_out"])
+
+
+@pytest.mark.parametrize("cdt", [BF16, ao.E4M3])
+def test_a_workspace_of_another_call_serves(m, kernel, cdt):
+    """One made for a long prompt (or for one token) is enough for every call; nothing is written behind it."""
+    H, Hq, D = 8, 64, 128
+    small = m.lsa_window_attention_workspace_size(4096, 1, Hq, H, D)
+    assert small < m.lsa_window_attention_workspace_size(64, 1, Hq, H, D)
+    for n, old in ((1, 3000), (64, 3000), (40, 9000), (200, 3000)):  # (6, 2, 3 parts and one)
+        c = Case([n], [old], H, Hq, D, 128, BF16, cdt)
+        d = c.cuda()
+        ws = torch.full((small + (8 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+        call(m, c, d, ws[:small])
+        m.lsa_check_device()
+        assert (ws[small:] == 0xA5).all()
+        check(c, d, rows={(0, 0), (0, n - 1)})
