@@ -358,7 +358,9 @@ lsa_status lsa_indexer_train_step(const void *h, const void *W_dq, const void *W
  *                The call writes powers of two: the least 2^e >= 2^-64 with amax <= 448 * 2^e over the
  *                page's new tokens of the head, or the scale that the page has where that is larger
  *                and the page already holds tokens; when the scale grows, the earlier codes are
- *                rounded again to it.  Infinite values saturate, NaN is stored as NaN.
+ *                rounded again to it.  Infinite values saturate, NaN is stored as NaN.  A page that holds
+ *                tokens under a negative, infinite or NaN scale is flagged and left as it is, for that head
+ *                and tensor.
  *   q_out        [N][H_q][D] dt: the rotated queries (may be q itself when q_stride = H_q * D)
  * D in {32, 64, 128}, page_size in {16, 32, 64, 128}, rot_dim a multiple of 16 up to D.  One launch,
  * no workspace.  A page that two new tokens' sequences share is written by both, in no fixed order.

@@ -375,9 +375,11 @@ __device__ __forceinline__ void append_page(const AppendArgs &A, int64_t job, Se
     for (int wi = 0; wi < APPEND_THREADS / 32; wi++) amax = fmaxf(amax, red[wi]);
     float now = e4m3_scale(amax);
     if (held) {
-        if (!(before >= 0.f) || before > 3.4028235e38f) {
+        if (!(before >= 0.f) || before > 3.4028235e38f) {  // (what the page's codes mean is not known: nothing is written)
             if (threadIdx.x == 0) flag(ERRF_SCALE);
-        } else if (before >= now) {
+            return;
+        }
+        if (before >= now) {
             now = before;
         } else {
             const float f = before / now;
