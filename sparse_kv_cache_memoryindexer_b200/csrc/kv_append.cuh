@@ -135,25 +135,39 @@ struct SeqOf {
 };
 
 // The sequences of tokens n .. n + many - 1 (b = -1: none, a row behind the last sequence) into slots.  Every thread
-// of the block calls it; one round of loads.
+// of the block calls it; one round of loads.  Where offsets decrease (flagged), sequences overlap: a token then is the
+// last one's that has it.
 __device__ __forceinline__ void block_seqs_of_tokens(const int64_t *q_offsets, const int32_t *cache_len, int B, int64_t N, int64_t n,
                                                      int many, SeqOf *slots)
 {
     if ((int)threadIdx.x < many) slots[threadIdx.x].b = -1;
+    int overlap = 0;
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const int64_t lo = __ldg(q_offsets + b), hi = __ldg(q_offsets + b + 1);
         const int len = __ldg(cache_len + b);
         if (lo < 0 || hi < lo || hi > N) {
             flag(ERRF_OFFSETS);
-        } else {  // (a token has one sequence, unless the offsets overlap: then any)
+        } else {
             for (int64_t i = max(lo, n); i < min(hi, n + many); i++) {
                 SeqOf &s = slots[i - n];
+                overlap |= atomicMax(&s.b, b) >= 0;
                 s.off = lo;
                 s.n = hi - lo;
                 s.len = len;
-                s.b = b;
             }
+        }
+    }
+    if (!__syncthreads_or(overlap)) return;
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {  // (several have written a slot: now the one whose it is)
+        const int64_t lo = __ldg(q_offsets + b), hi = __ldg(q_offsets + b + 1);
+        if (lo < 0 || hi < lo || hi > N) continue;
+        for (int64_t i = max(lo, n); i < min(hi, n + many); i++) {
+            SeqOf &s = slots[i - n];
+            if (s.b != b) continue;
+            s.off = lo;
+            s.n = hi - lo;
+            s.len = __ldg(cache_len + b);
         }
     }
     __syncthreads();

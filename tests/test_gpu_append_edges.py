@@ -45,3 +45,35 @@ def test_append_leaves_a_page_with_a_bad_scale(m, bad, n):
         d[t][pg, 1] = e[t][pg, 1] if t.startswith("v") else d[t][pg, 1]
         assert torch.equal(d[t].view(torch.uint8), e[t].view(torch.uint8)), t
     assert torch.equal(d["q_out"], e["q_out"])
+
+
+@pytest.mark.parametrize("B", [3, 400])
+def test_append_with_offsets_that_decrease(m, B):
+    """Offsets that go back are flagged; a token that two sequences then claim goes to the last one's place, whole, and no
+    other slot is touched.  (400 sequences: more than a block has threads, the last ones empty.)"""
+    from sparse_kv_cache_memoryindexer_b200 import LSAError
+    old = [7, 3, 9] + [1] * (B - 3)
+    c = Case(new=[5, 2, 5] + [0] * (B - 3), old=old, H=2, Hq=2, D=64, page=16)
+    d = c.cuda()
+    offs = torch.tensor([0, 5, 3, 8] + [8] * (B - 3))  # sequence 0: tokens 0 .. 4; 1: none, bad; 2: tokens 3 .. 7
+    d["q_offsets"].copy_(offs)
+    for _ in range(3):
+        m.lsa_kv_append(**d)
+        with pytest.raises(LSAError, match="offsets"):
+            m.lsa_check_device()
+        for t, cache in (("k", c.kc), ("v", c.vc)):
+            want = cache.clone()
+            src = c.parts()[1 if t == "k" else 2]
+            for n in range(8):
+                b = 0 if n < 3 else 2
+                p = old[b] + n - int(offs[b])
+                pg, sl = int(c.table[b, p // 16]), p % 16
+                got = d[t + "_cache"][pg, :, sl].cpu()
+                if t == "v":
+                    assert torch.equal(got, src[n]), n
+                else:
+                    y, mag = ao.rotate(src[n].double(), p, c.inv_freq, False)
+                    err = mag * ao.ROTATION
+                    assert ((got.double() - y).abs() <= err + ao.half_step(c.dt) * (y.abs() + err)).all(), n
+                want[pg, :, sl] = got
+            assert torch.equal(d[t + "_cache"].cpu(), want)
