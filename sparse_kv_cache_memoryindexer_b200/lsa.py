@@ -486,9 +486,10 @@ def _cache(what, q_offsets, cache_len, page_table, k_cache, v_cache, k_scale, v_
     return B, page_table.size(1), n_pages, H, page, D, code
 
 
-# (torch.cuda.current_stream() and current_device() without the objects and checks around them)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (torch.cuda.current_stream() and current_device() without the objects and checks around them, where torch has these
+# names: they are its own, and a build without CUDA has none)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _ptr(t):
