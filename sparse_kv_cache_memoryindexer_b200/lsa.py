@@ -496,6 +496,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _sees(window, n_sink):
+    """window and n_sink travel as C ints, which ctypes cuts without a word."""
+    if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= n_sink < 1 << 31):
+        raise ValueError(f"window and n_sink must be below 2^31, got {window} and {n_sink}")
+
+
 def _on(dev, stream, f, *args):
     """The C call with the tensors' device current, on `stream` (default: that device's current stream)."""
     st = _raw_stream(dev) if stream is None else _stream(stream)
@@ -595,6 +601,7 @@ def lsa_window_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, 
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_window_attention", q_offsets, cache_len, page_table, k_cache,
                                                       v_cache, k_scale, v_scale)
     code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
+    _sees(window, n_sink)
     dev = q.get_device()
     if not (dev >= 0
             and q_offsets.get_device() == dev and q_offsets.is_contiguous()
@@ -632,6 +639,7 @@ def lsa_core_attention(q, q_offsets, cache_len, page_table, k_cache, v_cache, to
     B, max_pages, n_pages, H, page, D, ccode = _cache("lsa_core_attention", q_offsets, cache_len, page_table, k_cache,
                                                       v_cache, None, None)
     code, N, Hq, sq = _attention_rows(q, D, out, lse_out)
+    _sees(window, n_sink)
     if ccode != code:
         raise TypeError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
     if topk_idx.dtype != torch.int32 or idx.dtype != torch.int32 or count.dtype != torch.int32:

@@ -28,3 +28,23 @@ print("loaded")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "loaded" in r.stdout, r.stderr[-2000:]
+
+
+def tensors():
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    return dict(q=bf(4, 8, 64), q_offsets=torch.zeros(3, dtype=torch.int64), cache_len=i32(2), page_table=i32(2, 5),
+                k_cache=bf(9, 2, 16, 64), v_cache=bf(9, 2, 16, 64), out=bf(4, 8, 64),
+                workspace=torch.zeros(256, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("over", [dict(window=1 << 31), dict(n_sink=1 << 31), dict(window=(1 << 32) + 5), dict(n_sink=-(1 << 32))])
+def test_windows_that_do_not_fit_a_c_int(over):
+    """They would be cut: a window of 2^32 + 5 to 5."""
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        lsa.lsa_window_attention(**tensors(), **over)
+    sel = dict(topk_idx=torch.zeros((4, 7), dtype=torch.int32), idx=torch.zeros(30, dtype=torch.int32),
+               count=torch.zeros(2, dtype=torch.int32), seq_offsets=torch.zeros(3, dtype=torch.int64), total_S=30,
+               hot_kv=torch.zeros((30, 512), dtype=torch.uint8))
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        lsa.lsa_core_attention(**tensors(), **sel, **over)
