@@ -203,6 +203,16 @@ class IndexerPath:
         self.attn_lse = torch.empty((self.B, H_q), dtype=torch.float32, device=dev)
         self.one_each = torch.arange(self.B + 1, dtype=torch.int64, device=dev)
 
+    def _check_window_entries(self, win_K, win_count, win_kv):
+        """The Top-k picks among the entries compressed in the window; core attention then needs every one's row."""
+        W = win_K.size(1)
+        if W == 0:
+            return
+        if win_count is None or win_kv is None or win_kv.dim() < 2 or win_kv.size(1) < W:
+            raise ValueError(f"win_K holds {W} entries a sequence: win_count and win_kv [B][{W}][row_bytes] go with it")
+        if W > self.W:
+            raise ValueError(f"win_K holds {W} entries a sequence, open_decode was told of {self.W}")
+
     def decode_step(self, q_step, w_step, q, k, v, seq_offsets, win_K=None, win_scale=None, win_count=None, win_kv=None,
                     inv_freq=None, interleaved=False, softmax_scale=None, stream=None):
         """One decode step of every sequence: the Lightning Top-k of its indexer query over the fetched entries
@@ -211,6 +221,8 @@ class IndexerPath:
         window and the first tokens.  Returns attn_out [B][H_q][D] (step_idx, attn_lse beside it); cache.advance
         follows once every layer is done.  Launches only kernels: a step can be recorded in a CUDA graph."""
         c = self.cache
+        if win_K is not None:
+            self._check_window_entries(win_K, win_count, win_kv)
         with _stage("lsa.lightning_topk_step"):
             lsa.lsa_lightning_topk_step(q_step, w_step, self.hot_K, self.hot_scale, self.idx, self.count, seq_offsets,
                                         self.total_S, self.k, self.step_idx, self.ws_step, win_K=win_K,

@@ -48,3 +48,30 @@ def test_windows_that_do_not_fit_a_c_int(over):
                hot_kv=torch.zeros((30, 512), dtype=torch.uint8))
     with pytest.raises(ValueError, match="below 2\\^31"):
         lsa.lsa_core_attention(**tensors(), **sel, **over)
+
+
+def test_decode_step_wants_the_rows_of_the_windows_entries(monkeypatch):
+    """Keys of entries compressed in the window without their rows would be picked, and then left out of the softmax."""
+    from sparse_kv_cache_memoryindexer_b200 import pipeline
+    path = object.__new__(pipeline.IndexerPath)
+    path.cache, path.W = None, 5
+    K, n = torch.zeros((2, 5, 32)), torch.zeros(2, dtype=torch.int32)
+    rows = lambda w: torch.zeros((2, w, 1024), dtype=torch.uint8)  # noqa: E731
+    step = lambda **kw: path.decode_step(None, None, None, None, None, None, **kw)  # noqa: E731
+    for kw in (dict(win_K=K, win_count=n), dict(win_K=K, win_count=n, win_kv=rows(4)), dict(win_K=K, win_kv=rows(5)),
+               dict(win_K=K, win_count=n, win_kv=rows(0))):
+        with pytest.raises(ValueError, match="go with it"):
+            step(**kw)
+    with pytest.raises(ValueError, match="was told of 5"):
+        step(win_K=torch.zeros((2, 6, 32)), win_count=n, win_kv=rows(6))
+    # what fits goes on to the calls (here: stopped at the first)
+    class Reached(Exception):
+        pass
+
+    def reached(name):
+        raise Reached
+    monkeypatch.setattr(pipeline, "_stage", reached)
+    for kw in (dict(), dict(win_K=K, win_count=n, win_kv=rows(5)), dict(win_K=K[:, :3], win_count=n, win_kv=rows(5)),
+               dict(win_K=K[:, :0], win_count=n), dict(win_kv=rows(5))):
+        with pytest.raises(Reached):
+            step(**kw)
