@@ -35,8 +35,15 @@ class WindowCache:
 
     def __init__(self, B, H_kv, D, page_size, n_pages, max_pages, dtype, cdtype=None, window=0, n_sink=0, device="cuda"):
         dev = torch.device(device)
+        cdtype = dtype if cdtype is None else cdtype
+        # what the calls would refuse, before anything is allocated for it
+        if D not in (32, 64, 128) or page_size not in (16, 32, 64, 128):
+            raise ValueError(f"D must be 32, 64 or 128 and page_size 16, 32, 64 or 128, got {D} and {page_size}")
+        if (dtype, cdtype) not in ((torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
+                                   (torch.bfloat16, torch.float8_e4m3fn)):
+            raise TypeError(f"dtype and cdtype must be fp32 and fp32, or bf16 and bf16 or float8_e4m3fn, got {dtype} and {cdtype}")
         self.B, self.H_kv, self.D, self.page_size = B, H_kv, D, page_size
-        self.dtype, self.cdtype, self.window, self.n_sink = dtype, dtype if cdtype is None else cdtype, window, n_sink
+        self.dtype, self.cdtype, self.window, self.n_sink = dtype, cdtype, window, n_sink
         shape = (n_pages, H_kv, page_size, D)
         self.k = torch.empty(shape, dtype=self.cdtype, device=dev)
         self.v = torch.empty(shape, dtype=self.cdtype, device=dev)
@@ -190,6 +197,8 @@ class IndexerPath:
             raise ValueError(f"the fetched rows ({self.row_bytes} bytes) must be [2][H_kv][D] of the cache's type")
         if cache.B != self.B:
             raise ValueError(f"the cache holds {cache.B} sequences, the path {self.B}")
+        if H_q <= 0 or H_q % cache.H_kv or not 1 <= self.k <= lsa.LSA_MAX_TOPK:
+            raise ValueError(f"H_q must be a multiple of H_kv and k in [1, {lsa.LSA_MAX_TOPK}], got {H_q} of {cache.H_kv} and {self.k}")
         self.cache, self.H_q, self.W = cache, H_q, W
         u8 = torch.uint8
         self.step_idx = torch.empty((self.B, self.k), dtype=torch.int32, device=dev)

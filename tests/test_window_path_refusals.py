@@ -75,3 +75,30 @@ def test_decode_step_wants_the_rows_of_the_windows_entries(monkeypatch):
                dict(win_K=K[:, :0], win_count=n), dict(win_kv=rows(5))):
         with pytest.raises(Reached):
             step(**kw)
+
+
+def test_window_cache_refuses_what_its_calls_would():
+    from sparse_kv_cache_memoryindexer_b200 import WindowCache
+    bf, f32, e4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    make = lambda D=64, page=16, dt=bf, cdt=None: WindowCache(2, 2, D, page, 4, 4, dt, cdt, device="cpu")  # noqa: E731
+    for kw in (dict(D=256), dict(D=96), dict(D=16), dict(page=8), dict(page=48), dict(page=256)):
+        with pytest.raises(ValueError, match="D must be"):
+            make(**kw)
+    for kw in (dict(dt=torch.float16), dict(dt=f32, cdt=bf), dict(dt=f32, cdt=e4), dict(dt=bf, cdt=f32), dict(dt=e4)):
+        with pytest.raises(TypeError, match="dtype and cdtype"):
+            make(**kw)
+    for kw in (dict(), dict(D=32), dict(D=128, page=128), dict(dt=f32), dict(cdt=e4)):
+        make(**kw)
+
+
+def test_open_decode_refuses_heads_and_lists_that_the_step_would():
+    from sparse_kv_cache_memoryindexer_b200 import WindowCache, pipeline
+    path = object.__new__(pipeline.IndexerPath)
+    path.B, path.row_bytes, path.k, path.idx = 2, 2 * 2 * 64 * 2, 16, torch.zeros(4, dtype=torch.int32)
+    cache = WindowCache(2, 2, 64, 16, 4, 4, torch.bfloat16, device="cpu")
+    for H_q in (0, 3, -2):
+        with pytest.raises(ValueError, match="multiple of H_kv"):
+            path.open_decode(cache, H_q)
+    path.k = 5000
+    with pytest.raises(ValueError, match="k in"):
+        path.open_decode(cache, 4)
