@@ -232,6 +232,11 @@ class IndexerPath:
         c = self.cache
         if win_K is not None:
             self._check_window_entries(win_K, win_count, win_kv)
+        dev = c.k.get_device()
+        if dev != lsa._current_device():  # (the Top-k runs on the current device)
+            with torch.cuda.device(dev):
+                return self.decode_step(q_step, w_step, q, k, v, seq_offsets, win_K, win_scale, win_count, win_kv,
+                                        inv_freq, interleaved, softmax_scale, stream)
         with _stage("lsa.lightning_topk_step"):
             lsa.lsa_lightning_topk_step(q_step, w_step, self.hot_K, self.hot_scale, self.idx, self.count, seq_offsets,
                                         self.total_S, self.k, self.step_idx, self.ws_step, win_K=win_K,

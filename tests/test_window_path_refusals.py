@@ -50,11 +50,51 @@ def test_windows_that_do_not_fit_a_c_int(over):
         lsa.lsa_core_attention(**tensors(), **sel, **over)
 
 
+def on_device(number):
+    """Stands in for a WindowCache on a CUDA device."""
+    class Cache:
+        class k:
+            get_device = staticmethod(lambda: number)
+    return Cache
+
+
+def test_decode_step_makes_the_caches_device_current(monkeypatch):
+    """All three calls run there, whichever device is current; the one that was is so again."""
+    from contextlib import contextmanager
+
+    from sparse_kv_cache_memoryindexer_b200 import pipeline
+    path = object.__new__(pipeline.IndexerPath)
+    path.cache, now, seen = on_device(1), [0], []
+
+    @contextmanager
+    def device(d):
+        before, now[0] = now[0], d
+        yield
+        now[0] = before
+
+    class Reached(Exception):
+        pass
+
+    @contextmanager
+    def stage(name):
+        seen.append((name, now[0]))
+        raise Reached
+        yield
+
+    monkeypatch.setattr(lsa, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(pipeline, "_stage", stage)
+    with pytest.raises(Reached):
+        path.decode_step(*[None] * 6)
+    assert seen == [("lsa.lightning_topk_step", 1)]
+
+
 def test_decode_step_wants_the_rows_of_the_windows_entries(monkeypatch):
     """Keys of entries compressed in the window without their rows would be picked, and then left out of the softmax."""
     from sparse_kv_cache_memoryindexer_b200 import pipeline
     path = object.__new__(pipeline.IndexerPath)
-    path.cache, path.W = None, 5
+    path.cache, path.W = on_device(0), 5
+    monkeypatch.setattr(lsa, "_current_device", lambda: 0)
     K, n = torch.zeros((2, 5, 32)), torch.zeros(2, dtype=torch.int32)
     rows = lambda w: torch.zeros((2, w, 1024), dtype=torch.uint8)  # noqa: E731
     step = lambda **kw: path.decode_step(None, None, None, None, None, None, **kw)  # noqa: E731
