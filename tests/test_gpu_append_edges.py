@@ -77,3 +77,32 @@ def test_append_with_offsets_that_decrease(m, B):
                     assert ((got.double() - y).abs() <= err + ao.half_step(c.dt) * (y.abs() + err)).all(), n
                 want[pg, :, sl] = got
             assert torch.equal(d[t + "_cache"].cpu(), want)
+
+
+def test_append_angles_are_not_rounded_to_fp32(m):
+    """At angles next to a quarter turn the cosine is small, and its error shows how far off the angle is: a reduced angle
+    rounded to fp32 (2^-25 of a half turn, 9e-8) would leave 1e-5 of a cosine of 0.01.  The cosine itself is within 2 ulp
+    (2^-22), what puts the rounding back adds half an ulp, and the product in fp64 of a thousand positions leaves 1e-12."""
+    H, D, page, n = 1, 128, 16, 200
+    c = Case(new=[n], old=[900], H=H, Hq=1, D=D, page=page, dt=torch.float32)
+    j = torch.arange(D // 2, dtype=torch.float64)
+    c.inv_freq = ((math.pi * (150 + j) + math.pi / 2 + 0.002 + 0.008 * (j % 17) / 17) / 1000).float()
+    for half, want in ((0, torch.cos), (1, torch.sin)):
+        c.fused.zero_()
+        c.fused[:, :, half * (D // 2):half * (D // 2) + D // 2] = 1.0
+        d = c.cuda()
+        m.lsa_kv_append(**d)
+        m.lsa_check_device()
+        a = (900 + torch.arange(n, dtype=torch.float64))[:, None] * c.inv_freq.double()[None]
+        cos = torch.cos(a)
+        got = d["q_out"][:, 0].cpu().double()
+        # x = (1, 0): (cos, sin);  x = (0, 1): (-sin, cos)
+        y = got[:, :D // 2] if half == 0 else got[:, D // 2:]
+        p = torch.arange(900, 900 + n)
+        k = d["k_cache"][c.table[0].long()[p // page], 0, p % page].cpu().double()
+        yk = k[:, :D // 2] if half == 0 else k[:, D // 2:]
+        near = (cos.abs() < 0.02) & (cos.abs() > 1e-3)
+        assert near.sum() >= 64
+        for v in (y, yk):
+            assert ((v - cos).abs()[near] <= (2.0 ** -22 + 2.0 ** -24) * cos.abs()[near] + 1e-12).all()
+            assert ((v - cos).abs() <= 2.0 ** -22).all()
