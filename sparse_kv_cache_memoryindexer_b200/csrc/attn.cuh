@@ -81,9 +81,23 @@ __device__ __forceinline__ bool good_scale(float s) { return s == 0.f || (s >= 7
 // outside is rare, and rows that it touches are done again by attend_row, which keeps the two maxima apart:
 //   - a scale outside (values beyond 2^48 or whose largest is below 2^-55): every row of the tile that met it;
 //   - a scale of zero counts as 2^-64 in the sum and as nothing in the value product, which is right unless its keys set m'
-//     (then the others' p' may have vanished): the rows whose maximum is such a key's.
-__device__ __forceinline__ bool odd_value_scale(float s) { return s != 0.f && (s < 5.421010862427522e-20f || s > 1.099511627776e12f); }
+//     (then the others' p' may have vanished).  Such a key's p' / vs is 2^64 times the factor of p', so only rows whose sum
+//     comes to that are concerned (from_zero), in a tile that met a scale of zero.
+// Both are looked at where a page's scale is read and at a tile's end, not for every key: a running maximum of the
+// zero-scale keys in the loops cost 6 %.
+__device__ __forceinline__ bool usual_value_scale(float s) { return s >= 5.421010862427522e-20f && s <= 1.099511627776e12f; }
 constexpr float ZERO_LV = -64.f, ZERO_INV = 18446744073709551616.f;  // log2 and reciprocal that a scale of zero counts with
+constexpr uint32_t MET_ZERO = 1u, MET_ODD = 2u;                      // what a tile's pages held
+
+__device__ __forceinline__ uint32_t met_of(float s) { return s == 0.f ? MET_ZERO : (good_scale(s) ? MET_ODD : 0u); }
+
+// The sum l of a row (or of a part) whose tile met `met`, as it is handed on: NaN for an odd scale; negative where the
+// maximum may be that of a key with a scale of zero (factor: of p').
+__device__ __forceinline__ float marked_sum(float l, uint32_t met, float factor)
+{
+    if (met & MET_ODD) return NAN;
+    return (met & MET_ZERO) && l >= 0.5f * ZERO_INV * factor ? -l : l;
+}
 
 // Key and value rows of one cached token of head h, with their page's scales (false: the page is bad, flagged).
 template <int CT>
@@ -151,7 +165,7 @@ __device__ __forceinline__ bool listed_rows(const AttnArgs &A, int b, int h, int
 // scores, D / 32 dimensions per lane for the values.  The way out for rows whose tile met an infinity or NaN: a
 // matrix product carries one from a key that a row must not see into that row as 0 x inf.  Such a row comes out
 // as NaN, so a row that is not finite is done again here, over its own keys alone.  So are rows of E4M3 caches that met
-// unusual value scales (odd_value_scale): the softmax sum is relative to the largest score (m), the value product to the
+// unusual value scales (usual_value_scale): the softmax sum is relative to the largest score (m), the value product to the
 // largest score + log2 vs (mo), whatever the scales.  And fp32 rows that are not finite: the split into two tf32 parts
 // makes NaN of an infinity (and of a number next to fp32's largest) that the row does see (CORE: with its Top-k entries).
 // qs: the warp's D floats of shared memory.

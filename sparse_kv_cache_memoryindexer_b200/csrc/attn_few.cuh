@@ -13,7 +13,7 @@
 //                own (elements 2^33 times smaller than the row's largest lose bits, no others).  A page's
 //                value scale vs enters the exponent: p' = 2^(s + log2 vs - m'), with m' the running maximum
 //                of s + log2 vs, so p' is rounded to f16 relative to what it adds to the output; the softmax sum
-//                takes p' / vs in fp32 (unusual scales: see odd_value_scale).  p' is kept 2^15 times larger (below
+//                takes p' / vs in fp32 (unusual scales: see usual_value_scale).  p' is kept 2^15 times larger (below
 //                f16's largest), so that only weights under 2^-29 of the largest are subnormal and lose bits.
 //   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
 //                (the fourth, lo lo, is below 2^-22 of the product).
@@ -55,8 +55,8 @@ struct Cfg {
     static constexpr float SHIFT = CT == DT_FP8 ? 15.f : 0.f;  // probabilities are kept 2^SHIFT times larger
     static constexpr int NT = D / 8;                // n-tiles of the value product
     static constexpr int QREGS = CT == DT_F32 ? D / 2 : D / 4;  // query fragment registers
-    static constexpr int OFF_ZMAX = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 32;
-    static constexpr int SMEM = OFF_ZMAX + (CT == DT_FP8 ? WARPS * ROWS * 4 : 0);
+    static constexpr int OFF_MET = RING + 2 * WARPS * ROWS * 4 + WARPS * STAGES * 32;
+    static constexpr int SMEM = OFF_MET + (CT == DT_FP8 ? WARPS * 4 : 0);
 };
 
 // 16-byte piece of a row that holds piece c of row `row`: chosen for each access pattern below so that the
@@ -560,13 +560,13 @@ __device__ __forceinline__ void tile_row(const AttnArgs &A, const Seq &s, const 
 }
 
 // A part in the workspace: maxima and sums of 16 rows (of 2^(x - max)), then the sums of values.  E4M3: a sum is negative
-// where the maximum is that of a key with a value scale of zero, NaN where a scale is unusual (odd_value_scale).
+// where the maximum is that of a key with a value scale of zero, NaN where a scale is unusual (marked_sum).
 template <int D>
 constexpr size_t part_floats() { return 2 * ROWS + (size_t)ROWS * D; }
 
 template <int CT>
 __device__ __forceinline__ float sum_of(float l) { return CT == DT_FP8 ? fabsf(l) : l; }
-// The part (m, l) sets the maximum M, with a key whose value scale is zero.
+// The part (m, l) sets the maximum M, perhaps with a key whose value scale is zero.
 template <int CT>
 __device__ __forceinline__ bool from_zero(float l, float m, float M) { return CT == DT_FP8 && l < 0.f && m == M; }
 
@@ -585,11 +585,10 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     struct Meta { float sc[2][2]; uint32_t live, pad[3]; };  // key and value scale of each half; which keys are there
     Meta *meta = (Meta *)(ml + 2 * WARPS * ROWS) + warp * C::STAGES;
     const uint32_t meta_a = (uint32_t)__cvta_generic_to_shared(meta);
-    // E4M3: each row's largest score of a key with a value scale of zero (with its ZERO_LV); infinite: an unusual scale
-    float *zmax = (float *)(smem + C::OFF_ZMAX) + warp * ROWS;
+    // E4M3: whether the warp met unusual value scales
+    uint32_t *met = (uint32_t *)(smem + C::OFF_MET) + warp;
     if constexpr (CT == DT_FP8) {
-        if (lane < ROWS) zmax[lane] = -INFINITY;
-        __syncwarp();
+        if (lane == 0) *met = 0;
     }
 
     int32_t *entries = (int32_t *)(smem + C::SMEM);  // CORE: rows of the part's Top-k entries
@@ -652,11 +651,12 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         if (i >= count) return -1;
         const int u = chunk_of(i);
         if (CORE && u >= s.chunks) return entries[(u - c0) * KEYS + (lane & 15)];
-        // (lanes 0-15 for the first half, the others for the second; its page may lie behind the table's end: there is none)
+        // (lanes 0-15 for the first half, the others for the second; its page may lie behind the table's end: not used)
         const int at = (pos_of(u) + (KH > 1 ? lane & 16 : 0)) >> A.page_shift;
-        if (KH > 1 && at >= A.max_pages) return -1;
-        return __ldg(A.page_table + (int64_t)b * A.max_pages + at);
+        return __ldg(A.page_table + (int64_t)b * A.max_pages + (KH > 1 ? min(at, A.max_pages - 1) : at));
     };
+    // (the last position to load: a length that is flagged may put rows behind the page table's end)
+    const int p_end = min(t.p_hi, (A.max_pages << A.page_shift) - 1);
     // start the loads of the CTA's i-th chunk (warp w takes w, w + WARPS, ..)
     auto issue = [&](int i, int stage, int32_t found) {
         const uint32_t kb = ring_a + (uint32_t)stage * C::CHUNK, vb = kb + KEYS * C::RB;
@@ -667,7 +667,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
             for (int hf = 0; hf < KH; hf++) {
                 const int p0 = pos_of(u) + 16 * hf;
                 int page = KH > 1 ? __shfl_sync(0xffffffffu, found, 16 * hf) : found;
-                if (KH > 1 && (p0 > t.p_hi || (p0 + 15 < low && p0 >= A.n_sink))) {
+                if (KH > 1 && (p0 > p_end || (p0 + 15 < low && p0 >= A.n_sink))) {
                     page = -1;  // (a half that no row sees: its page is not looked at)
                 } else if (page < 0 || page >= A.n_pages) {
                     if (lane == 0) flag(ERRF_PAGE);
@@ -676,7 +676,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 const int64_t ph = (int64_t)max(page, 0) * A.H + h;
                 const int64_t byte = ((ph << A.page_shift) + (p0 & ((1 << A.page_shift) - 1))) * C::RB + lane * 16;
                 const uint8_t *kp = (const uint8_t *)A.k_cache + byte, *vp = (const uint8_t *)A.v_cache + byte;
-                if (page >= 0 && p0 + 15 <= t.p_hi && (p0 >= low || p0 + 16 <= A.n_sink)) {
+                if (page >= 0 && p0 + 15 <= p_end && (p0 >= low || p0 + 16 <= A.n_sink)) {
 #pragma unroll
                     for (int x = 0; x < XH; x++) cp_async16(kb + dst(hf * XH + x), kp + 512 * x, 16);
 #pragma unroll
@@ -685,7 +685,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
 #pragma unroll
                     for (int x = 0; x < XH; x++) {
                         const int pos = p0 + (lane + 32 * x) / PR;
-                        const bool see = page >= 0 && pos <= t.p_hi && (pos >= low || pos < A.n_sink);
+                        const bool see = page >= 0 && pos <= p_end && (pos >= low || pos < A.n_sink);
                         cp_async16(kb + dst(hf * XH + x), see ? kp + 512 * x : (const uint8_t *)A.k_cache, see ? 16 : 0);
                         cp_async16(vb + dst(hf * XH + x), see ? vp + 512 * x : (const uint8_t *)A.v_cache, see ? 16 : 0);
                     }
@@ -758,11 +758,13 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                 }
                 if (vs != last_vs[hf]) {
                     last_vs[hf] = vs;
-                    lv[hf] = vs > 0.f ? log2f(vs) : ZERO_LV;
-                    inv_vs[hf] = vs > 0.f ? 1.f / vs : ZERO_INV;
-                    if (good_scale(vs) && odd_value_scale(vs)) {
-                        if (lane < ROWS) zmax[lane] = INFINITY;
-                        __syncwarp();
+                    if (usual_value_scale(vs)) {
+                        lv[hf] = log2f(vs);
+                        inv_vs[hf] = 1.f / vs;
+                    } else {
+                        lv[hf] = vs > 0.f ? log2f(vs) : ZERO_LV;
+                        inv_vs[hf] = vs > 0.f ? 1.f / vs : ZERO_INV;
+                        if (lane == 0 && (live >> (16 * hf) & 1)) *met |= met_of(vs);
                     }
                 }
             }
@@ -793,24 +795,6 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                                      (listed || (pos <= me && (A.window == 0 || pos > me - A.window || pos < A.n_sink)));
                     if (!see) x[j][e] = -INFINITY;
                 }
-        }
-        if constexpr (CT == DT_FP8) {
-            bool zero = false;
-#pragma unroll
-            for (int hf = 0; hf < KH; hf++) zero |= (live >> (16 * hf) & 1) && last_vs[hf] == 0.f;
-            if (zero) {
-#pragma unroll
-                for (int i2 = 0; i2 < 2; i2++) {
-                    float zm = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 2 * KH; j++)
-                        if (last_vs[j / 2] == 0.f) zm = fmaxf(zm, fmaxf(x[j][2 * i2], x[j][2 * i2 + 1]));
-                    zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
-                    zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 2));
-                    if (c == 0) zmax[r + 8 * i2] = fmaxf(zmax[r + 8 * i2], zm);
-                }
-                __syncwarp();
-            }
         }
         bool moved = false;
         float f[2];
@@ -858,6 +842,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         fill = fill + 1 == C::STAGES ? 0 : fill + 1;
     }
     cp_wait<0>();
+    __syncwarp();
 
     // join the warps: maxima, then every warp's sums brought to the common maximum
 #pragma unroll
@@ -865,11 +850,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         if (c == 0) {
-            if constexpr (CT == DT_FP8) {
-                const float zm = zmax[r + 8 * i];
-                if (zm == INFINITY) l[i] = NAN;
-                else if (zm == m[i] && zm != -INFINITY) l[i] = -l[i];
-            }
+            if constexpr (CT == DT_FP8) l[i] = marked_sum(l[i], *met, 32768.f);
             ml[warp * ROWS + r + 8 * i] = m[i];
             ml[(WARPS + warp) * ROWS + r + 8 * i] = l[i];
         }
@@ -890,7 +871,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
     __syncthreads();
     constexpr int GROUPS = D / 4;  // four dimensions of a row each
     uint32_t bad = 0;              // rows of this thread's that are not finite
-    // (again: the row's maximum is that of a key with a value scale of zero)
+    // (again: the row's maximum may be that of a key with a value scale of zero)
     auto write = [&](int row, int d, float4 o, float M, float L, bool again) {
         int n, pos, g;
         tile_row<CORE>(A, s, t, row, n, pos, g);

@@ -69,7 +69,7 @@ struct Cfg {
 constexpr float STALE = 8.f;  // log2 of how far a row's maximum may run ahead of the one in use
 
 // Page data of a block: for each 16 keys the key scale, log2 of the value scale and its reciprocal; which are live,
-// and which have a value scale of zero (bit 8: some page has an unusual one, see odd_value_scale).
+// and which have a value scale of zero.
 struct Meta {
     float ks[8], lv[8], inv[8];
     uint32_t live, zero, pad[2];
@@ -191,7 +191,7 @@ __device__ __forceinline__ void row_of(const AttnArgs &A, const Job &j, int r, i
 }
 
 // A part in the workspace: maxima (log2, of what the exponents are relative to) and sums of 256 rows, then O.  E4M3: a
-// sum is negative where the maximum is that of a key with a value scale of zero, NaN where a scale is unusual.
+// sum is marked where value scales are unusual (marked_sum).
 template <int D>
 constexpr size_t part_floats() { return 2 * CTA_ROWS + (size_t)CTA_ROWS * D; }
 
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
     float *qfac = (float *)(base + C::OFF_QF);
     uint32_t *tmem_holder = (uint32_t *)(base + C::OFF_MISC);
     volatile int *abort_flag = (volatile int *)(base + C::OFF_MISC + 4);
+    uint32_t *met = (uint32_t *)(base + C::OFF_MISC + 8);  // unusual value scales of the CTA's pages (E4M3; the producer's)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * i; };
     auto k_full = [&](int s) { return bar(s); };
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         mbar_init(vraw_empty, 4);
         mbar_init(drained, 1);
         *abort_flag = 0;
+        *met = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) {
@@ -399,9 +401,6 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         // (a factor of zero would make NaN of a masked -inf)
         const float f = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1e-30f) * (FP8 ? qfac[r] : 1.f);
         const float fx = FP8 ? 1.f : f;  // from s to log2 units
-        // E4M3: the last maximum that a key with a value scale of zero has set; infinite: an unusual scale was met.  (In
-        // the row factor's place, which nobody else reads: a register less through the loop.)
-        if (FP8) qfac[r] = -INFINITY;
         float m = -INFINITY, l = 0.f;    // m: the maximum in use, in the units of s
         bool ok = true;
         for (int i = 0; i < nb; i++) {
@@ -444,16 +443,15 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     for (int k = 0; k < 32; k++) s[pc][k] = (w & (1u << k)) ? s[pc][k] : -INFINITY;
                 }
             }
-            float mx8[8];  // (of each 16 keys)
+            float mx4[4];
 #pragma unroll
-            for (int k8 = 0; k8 < 8; k8++) {
-                const float *x16 = &s[k8 / 2][16 * (k8 & 1)];
-                mx8[k8] = x16[0];
+            for (int pc = 0; pc < 4; pc++) {
+                mx4[pc] = s[pc][0];
 #pragma unroll
-                for (int k = 1; k < 15; k += 2) mx8[k8] = fmaxf(fmaxf(mx8[k8], x16[k]), x16[k + 1]);
-                mx8[k8] = fmaxf(mx8[k8], x16[15]);
+                for (int k = 1; k < 31; k += 2) mx4[pc] = fmaxf(fmaxf(mx4[pc], s[pc][k]), s[pc][k + 1]);
+                mx4[pc] = fmaxf(mx4[pc], s[pc][31]);
             }
-            const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             const bool grow = m == -INFINITY ? mx != -INFINITY : (mx - m) * fx > STALE;
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = fmaxf(m, mx);
@@ -474,13 +472,6 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     }
                     tmem_wait_st();
                 }
-            }
-            if (FP8 && me->zero) {
-                float zm = -INFINITY;
-#pragma unroll
-                for (int k8 = 0; k8 < 8; k8++) zm = fmaxf(zm, (me->zero >> k8 & 1) ? mx8[k8] : -INFINITY);
-                if (me->zero >> 8) qfac[r] = INFINITY;
-                else if (zm == m && qfac[r] != INFINITY) qfac[r] = m;
             }
             const float ref = (m == -INFINITY ? 0.f : m) * fx - C::SHIFT;
             float2 sum = make_float2(0.f, 0.f);
@@ -515,12 +506,10 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
         if (ok && !wait_warp(o_done(t), (nb - 1) & 1, abort_flag)) ok = false;
         if (ok) {
             tc_fence_after();
-            bool bad = false;
-            if constexpr (FP8) {
-                if (qfac[r] == INFINITY) l = NAN;
-                else bad = qfac[r] == m && m != -INFINITY && r < j.rows;
-            }
-            const bool zero = bad;
+            if (FP8) l = marked_sum(l, *met, 128.f);
+            bool bad = !part && r < j.rows && few::from_zero<CT>(l, m, m);
+            const float mark = l;
+            l = few::sum_of<CT>(l);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float ml2 = m * (FP8 ? 1.f : f) - C::SHIFT;
             const int64_t at = n * A.Hq + h * G + g;
@@ -552,12 +541,12 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
             if (r < j.rows) {
                 if (part) {
                     part[r] = m == -INFINITY ? -INFINITY : ml2;
-                    part[CTA_ROWS + r] = zero ? -l : l;
+                    part[CTA_ROWS + r] = mark;
                 } else if (A.lse) {
                     A.lse[at] = l == 0.f ? -INFINITY : (ml2 + log2f(l)) * 0.6931471805599453f;
                 }
             }
-            uint32_t again = part ? 0u : __ballot_sync(0xffffffffu, bad);
+            uint32_t again = __ballot_sync(0xffffffffu, bad);
             while (again) {  // (this tile's products are done: its query tile is free for the rows)
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
@@ -623,14 +612,13 @@ __global__ void __launch_bounds__((Cfg<CT, D>::THREADS), 1)
                     }
                 }
                 uint32_t live = 0, zero = 0;
-                {
-                    const uint32_t zs = __ballot_sync(0xffffffffu, page >= 0 && vs == 0.f);
-                    if (__any_sync(0xffffffffu, FP8 && page >= 0 && odd_value_scale(vs))) zero = 256u;
-                    for (int k = 0; k < 8; k++) {
-                        const int p = k * 16 / A.page;
-                        live |= (there >> p & 1u) << k;
-                        zero |= (zs >> p & 1u) << k;
-                    }
+                for (int k = 0; k < 8; k++) live |= (there >> (k * 16 / A.page) & 1u) << k;
+                const bool odd = FP8 && page >= 0 && !usual_value_scale(vs);
+                if (FP8 && __any_sync(0xffffffffu, odd)) {
+                    const uint32_t zs = __ballot_sync(0xffffffffu, odd && vs == 0.f);
+                    for (int k = 0; k < 8; k++) zero |= (zs >> (k * 16 / A.page) & 1u) << k;
+                    const uint32_t of = __reduce_or_sync(0xffffffffu, odd ? met_of(vs) : 0u);
+                    if (lane == 0) *met |= of;
                 }
                 if (lane == 0) {
                     me->live = live;
