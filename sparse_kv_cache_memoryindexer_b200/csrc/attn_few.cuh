@@ -1171,7 +1171,18 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attn_join(const AttnArgs A, 
 constexpr int SPLIT_CTAS = 3 * 148;
 inline size_t parts_bytes(int D) { return (size_t)2 * SPLIT_CTAS * (2 * ROWS + (size_t)ROWS * D) * sizeof(float); }
 
-// Tiles of at most this many keys go to clusters, where these are few enough to run at once.
+// Tiles of at most this many keys go to clusters, the others are split over the grid.  Measured (split : cluster, us, 8 heads
+// of 128 in bf16, a step, L2 cold):
+//   keys                               512       1000        2000       4000       8000
+//   1 user                           19 : 12    21 : 14    23 : 14    27 : 18    29 : 23
+//   32 users                         33 : 26    45 : 39    70 : 64   115 : 109  195 : 189
+//   100 users                        72 : 64   106 : 92   168 : 147  311 : 281  583 : 537
+//   32 users, one of that length,
+//   the others of 100 keys                      27 : 25    31 : 33    33 : 53    39 : 90
+// Clusters lead while lengths are alike, and lose to the even shares by what lengths differ: the more, the longer they are.
+// A length is not known here, only its bound, hence the limit.  E4M3 likewise (32 users 27 : 25, 29 : 35, 35 : 55, 43 : 96 in
+// the last row); fp32 at D = 128, one CTA an SM, is within 6 % either way over windows (32 users of 4000: 428 : 443), but
+// its Top-k lists lose by clusters of eight, which do not fill the SMs (8 users, Top-2048: 74 : 104).
 constexpr int64_t CLUSTER_KEYS = 4096;
 
 template <int QT, int CT, int D, bool CORE>
@@ -1198,7 +1209,9 @@ cudaError_t launch(const AttnArgs &A, void *workspace, int sms, cudaStream_t st,
         // as many CTAs a tile as leave each one chunk a warp and run at once
         int Z = 1;
         while (Z < 8 && 2 * Z * WARPS <= chunks + WARPS - 1 && 2 * Z * likely * A.H <= per_sm * sms) Z *= 2;
-        // (not where the last of several waves would leave more than a quarter of the CTAs' time unused)
+        // (not where the last of several waves would leave more than a quarter of the CTAs' time unused: 64 users, 8 heads of
+        // 64, 512 tiles on 444 places: 2000 keys 74 : 73, 4000 keys 119 : 129, E4M3 94 : 109; up to 1024 keys the second
+        // launch costs more than that)
         const int64_t ctas = Z * likely * A.H, slots = (int64_t)per_sm * sms;
         if (chunks * KEYS <= 1024 || ctas <= slots || 4 * ctas >= 3 * ((ctas + slots - 1) / slots) * slots) {
             auto kernel = k_attn_few<QT, CT, D, CORE, false>;

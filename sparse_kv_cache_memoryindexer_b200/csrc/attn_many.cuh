@@ -954,12 +954,20 @@ inline bool make_cache_map(CUtensorMap *m, const void *ptr, bool fp8, int64_t ro
 }
 
 // Whether this kernel takes the call: its MMAs and tensor maps can hold it, and it is the faster one.  Estimates in
-// microseconds from measurements at D = 128: the few-row kernel 8 and 1.45 (E4M3: 1.12) for each 16-key chunk of a 16-row
-// tile that falls on one of the SM's 8 warps, this one 5 and 1.8 (2.2) for each block of its longest CTA.  Measured (few-row
-// kernel : this one, bf16; E4M3): 32 users, window 4096, 8 heads: 16 rows 98 : 140, 77 : 174; 32 rows 181 : 141,
-// 138 : 175; 64 rows 315 : 141, 259 : 176.  One user, 8 heads, window 512, 128 rows: 12 : 18, 13 : 24.  One user, one
-// head, 131072 keys: 64 rows 45 : 51, 47 : 61; 128 rows 62 : 52, 68 : 64.  LSA_ATTN_MANY=0 or 1 in the environment takes
-// the one or the other wherever it can (to check them against one another).
+// microseconds from measurements: the few-row kernel 8 and, for each 16-key chunk of a 16-row tile that falls on one of the
+// SM's 8 warps, 1.45 (E4M3: 1.12) at D = 128 and 0.8 (0.9) at D = 64; this one 5 and 1.95 (2.2) for each block of its longest
+// CTA, whose softmax does not know D.  Measured (few-row kernel : this one; 9000 tokens before, L2 cold):
+//                                              D = 128 bf16    E4M3         D = 64 bf16    E4M3
+//   32 users, window 4096, 8 heads, 16 rows    121 : 150       83 : 180     74 : 144       60 : 176
+//   the same, 32 rows                          207 : 150      143 : 181     95 : 146       98 : 176
+//   the same, 64 rows                          326 : 150      258 : 184    165 : 146      172 : 177
+//   8 users, window 1024, 8 heads, 64 rows      28 : 31        29 : 37      23 : 31        25 : 35
+//   the same, 128 rows                          49 : 31        51 : 37      45 : 31        49 : 35
+//   1 user, window 512, 8 heads, 128 rows       17 : 23        17 : 27      14 : 22        15 : 25
+//   1 user, 131000 keys, 1 head, 64 rows        51 : 60        58 : 70      43 : 56        45 : 66
+//   the same, 128 rows                          70 : 61        74 : 72      53 : 59        55 : 68
+//   2 users, 1000 keys, 4 heads, 800 rows       53 : 33        56 : 40      25 : 31        27 : 37
+// LSA_ATTN_MANY=0 or 1 in the environment takes the one or the other wherever it can (to check them against one another).
 inline bool takes(const AttnArgs &A, int cdt, size_t workspace_bytes, int sms)
 {
     if (cdt == DT_F32 || A.k > 0 || (A.D != 64 && A.D != 128)) return false;
@@ -969,8 +977,9 @@ inline bool takes(const AttnArgs &A, int cdt, size_t workspace_bytes, int sms)
     const int64_t rows = std::max<int64_t>(A.N / A.B, 1) * (A.Hq / A.H), keys = likely_keys(A);
     int64_t blocks;
     splits_of(A.N, A.B, A.Hq, A.H, A.D, sms, keys / BLOCK + 1, workspace_bytes, &blocks);
-    const double few_us = 8 + (cdt == DT_FP8 ? 1.12 : 1.45) * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
-    const double many_us = 5 + (cdt == DT_FP8 ? 2.2 : 1.8) * blocks;
+    const double chunk_us = A.D == 64 ? (cdt == DT_FP8 ? 0.9 : 0.8) : (cdt == DT_FP8 ? 1.12 : 1.45);
+    const double few_us = 8 + chunk_us * A.B * ((rows + 15) / 16) * A.H * (keys / 16 + 1) / (8.0 * sms);
+    const double many_us = 5 + (cdt == DT_FP8 ? 2.2 : 1.95) * blocks;
     return ((env && env[0] == '1') || many_us < few_us) && tc_available();
 }
 
