@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import attn_oracle as ao
+import test_gpu_attention
 from test_gpu_attention import BF16, F32, Case, call, check
 
 pytestmark = pytest.mark.gpu
@@ -205,3 +206,13 @@ def test_a_workspace_of_another_call_serves(m, kernel, cdt):
         m.lsa_check_device()
         assert (ws[small:] == 0xA5).all()
         check(c, d, rows={(0, 0), (0, n - 1)})
+
+
+@pytest.mark.parametrize("test", ["strided_queries_and_no_lse", "large_scores_and_scale", "rows_with_nothing_to_see",
+                                  "bad_data_is_left_out_and_flagged", "zero_scales", "many_sequences", "negative_and_zero_scale",
+                                  "replayed_graph_follows_the_lengths", "two_streams_with_their_own_workspaces",
+                                  "the_same_bits_every_time", "pages_past_32_bits", "no_tokens_and_no_entries",
+                                  "bad_length_with_nan_ends"])
+def test_on_both_kernels(m, kernel, test):
+    """Each by itself, so that one's failure does not hide the next."""
+    getattr(test_gpu_attention, "test_" + test)(m)
