@@ -390,7 +390,9 @@ lsa_status lsa_kv_append(const void *q, int64_t q_stride, const void *k, int64_t
  *                computed key by key, which is right but slow)
  *   page_table   pages that no query sees are not looked at (they may have been given back)
  *   out          [N][H_q][D] dt; lse_out [N][H_q] fp32 (nullable)
- * Products and sums are fp32; probabilities enter the value product in bf16 (f16 for E4M3 caches).
+ * Products are exact, their sums and the softmax sum fp32; probabilities enter the value product in
+ * bf16 (f16 for E4M3 caches, whose queries are brought to f16 by a power of two).  fp32: every product
+ * is of two tf32 parts a factor, without the smallest of the four (off by 3 * 2^-22 of it at most).
  * Limits as lsa_kv_append; H_q a multiple of H_kv; max_pages * page_size below 2^31.  Bad lengths,
  * offsets, pages and scales are flagged, their keys left out.  out must not overlap q.
  * Kernels: tcgen05 for many query rows (bf16 and E4M3 caches, D = 64 or 128), warp MMAs for few; a

@@ -8,24 +8,28 @@
 // for another warp until the tile's end, where the warps' running maxima, sums and outputs are joined.
 // The products are warp MMAs: 16 rows are one m16 tile, and the tensor pipe is far from its limit here
 // (32 MMAs for the 8 KB of a bf16 chunk), so nothing is gained by staging them through TMEM.
-//   bf16 cache:  m16n8k16 bf16, probabilities rounded to bf16 (their sum is taken before that).
+//   bf16 cache:  m16n8k16 bf16, probabilities rounded to bf16 (their sum is taken before that): the product takes both
+//                operands in the values' type, and a second product for the rest of each probability would double it.  Costs
+//                2^-8 of a weight at most: output error 2.0e-3 to 2.3e-3 (2-norm) where the result's rounding has 1.7e-3.
 //   E4M3 cache:  codes decoded exactly to f16; the query row is brought to f16 by a power of two of its
-//                own (elements 2^33 times smaller than the row's largest lose bits, no others).  A page's
+//                own, its largest element to [2^8, 2^9).  f16 steps by 2^-24 at least, so a bf16 element keeps its eight bits
+//                down to 2^-17; from 2^25 below the largest they are lost, from 2^33 below the element is.  A page's
 //                value scale vs enters the exponent: p' = 2^(s + log2 vs - m'), with m' the running maximum
 //                of s + log2 vs, so p' is rounded to f16 relative to what it adds to the output; the softmax sum
 //                takes p' / vs in fp32 (unusual scales: see usual_value_scale).  p' is kept 2^15 times larger (below
 //                f16's largest), so that only weights under 2^-29 of the largest are subnormal and lose bits.
 //   fp32 cache:  m16n8k8 tf32 with both operands split into two parts, x = hi + lo, three products
-//                (the fourth, lo lo, is below 2^-22 of the product).
+//                (the fourth, lo lo, is below 2^-22 of the product, as is what the rounding of each lo leaves): there is no
+//                MMA in fp32.  Output error 7.7e-7 (2-norm) where sums in fp32 have 4.2e-7.  The split has no infinities: see attend_row.
 //
 // Measured: 32 users over a window of 4096, 8 heads of 128 in bf16: 96 us, 5.4 TB/s, bound by HBM; 8 histories of up
-// to 131071 tokens in E4M3: 225-239 us, 4.5-4.8 TB/s, bound by instruction issue; Top-2048 and a window of 512 for 32
-// users, 64 heads on 2: 41 us, bound by the 16-row tiles, which read a group's rows once for every 16 heads.
+// to 131071 tokens in E4M3: 242 us (231-248 by box), 4.4 TB/s, bound by instruction issue; Top-2048 and a window of 512 for
+// 32 users, 64 heads on 2: 42 us, bound by the 16-row tiles, which read a group's rows once for every 16 heads.
 //
 // Work is shared in one of two ways.  Tiles of bounded length (a window, a Top-k list) go to a cluster of up to
 // eight CTAs each, which share its chunks and join their sums through distributed shared memory: one launch.
-// Otherwise the chunks of all tiles of all sequences form one range that the CTAs share evenly, whatever the
-// lengths; a CTA's part of a tile that it does not hold whole goes to the workspace and k_attn_join adds the parts
+// Otherwise the chunks of all tiles of all sequences form one range that the CTAs share evenly (a tile's start and end, about
+// as long as a dozen chunks, are not counted: a CTA whose share is many short sequences takes longer); a CTA's part of a tile that it does not hold whole goes to the workspace and k_attn_join adds the parts
 // in order.  A CTA leaves at most two parts.
 //
 // The Top-k entries' rows are looked up by the CTA that reads them, before it reads: the sequence's ascending fetch

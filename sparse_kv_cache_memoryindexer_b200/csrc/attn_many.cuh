@@ -12,11 +12,15 @@
 // What bounds it: a tile's chain of softmax (about 2200 clocks beside the other tile's) and its two products (1000)
 // takes 3500 clocks a block, where the MMAs of both tiles take 2048 (2 x 128 x 128 x D multiply-adds each, 4096 a
 // clock) and their exponentials as long.  Two chunks of 4096 and 1900 tokens over a window of 4096, 32 heads of 128:
-// 530-565 us, 870-925 TFLOP/s (the plain form 42 ms); 2048 tokens on an E4M3 history of 14001: 574 us, 880 TFLOP/s.
+// 566 us, 865 TFLOP/s (the plain form 42 ms); 2048 tokens on an E4M3 history of 14001: 579 us, 870 TFLOP/s.
+//
+// Probabilities are rounded to the type of the values in the product, bf16 or f16, once (both operands of an MMA have one type);
+// their sum is taken before that, in fp32.
 //
 // Keys and values come by TMA, one box per page (128-byte swizzle); E4M3 pages come as they are and four warps
 // decode them exactly to f16 tiles (see attn_few.cuh for how a page's scales enter; the probabilities' factor
-// is 2^7 here, so that with a stale maximum they stay below f16's largest).
+// is 2^7 here, so that with a stale maximum they stay below f16's largest: weights under 2^-21 of the maximum in use are
+// subnormal in f16 and lose bits, where the few-row kernel, whose maximum is never stale, has 2^-29).
 // Value rows that none of the CTA's rows sees (behind its last token, before its first window, on pages that are
 // not there) are zeroed: what lies there, stale or never written, must not meet a probability of zero in the
 // product.  A key that some rows see and others must not, itself NaN or infinite, makes its tile's rows NaN;

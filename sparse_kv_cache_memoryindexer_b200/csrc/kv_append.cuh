@@ -16,9 +16,9 @@
 //
 // The work is one pass over the data and bound by HBM; a unit is 16 elements of a row (both partners of
 // eight pairs), so no thread needs another's values.  Rows that are stored as they are read go by token
-// (k_kv_append_rows); an E4M3 page and head is one CTA (its scale needs all its new values, held in
+// (append_rows); an E4M3 page and head is one CTA (its scale needs all its new values, held in
 // registers, and nobody else touches the page).  Both kinds of CTA share one launch.  16384 tokens of 64 + 16 heads of
-// 128 into a bf16 cache: 138 us, 5.7 TB/s; 8 ragged chunks into an E4M3 cache, 32 query heads: 74 us, 3.5 TB/s (bound by
+// 128 into a bf16 cache: 140 us, 5.6 TB/s; 8 ragged chunks into an E4M3 cache, 32 query heads: 74 us, 3.5 TB/s (bound by
 // instruction issue: the angles of a page's keys are formed for every head).
 #pragma once
 #include "common.cuh"
@@ -93,7 +93,7 @@ __device__ __forceinline__ void store_run8(void *row, int64_t e, const float (&x
 }
 
 // cos and sin of pos * inv_freq: of the reduced angle's fp32 value, then corrected by what that rounding left off
-// (d, to first order: d^2 is below 2^-48).
+// (d, to first order: h is within 2^-25 half turns of t, so d is below pi 2^-25 and what is left off, d^2 / 2, below 2^-47).
 __device__ __forceinline__ void turn(int64_t pos, float inv_freq, float &c, float &s)
 {
     double t = (double)pos * (double)inv_freq * 0.31830988618379067154;  // 1 / pi: half turns
