@@ -760,7 +760,8 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                     if (lane == 0) flag(ERRF_SCALE);
                     live &= ~(0xFFFFu << (16 * hf));
                 }
-                if (vs != last_vs[hf]) {
+                // (a half that is not there has come in with scales of zero, which are not a page's)
+                if ((live >> (16 * hf) & 1) && vs != last_vs[hf]) {
                     last_vs[hf] = vs;
                     if (usual_value_scale(vs)) {
                         lv[hf] = log2f(vs);
@@ -768,7 +769,7 @@ __device__ __forceinline__ void do_tile(const AttnArgs &A, const Seq &s, int b, 
                     } else {
                         lv[hf] = vs > 0.f ? log2f(vs) : ZERO_LV;
                         inv_vs[hf] = vs > 0.f ? 1.f / vs : ZERO_INV;
-                        if (lane == 0 && (live >> (16 * hf) & 1)) *met |= met_of(vs);
+                        if (lane == 0) *met |= met_of(vs);
                     }
                 }
             }

@@ -208,6 +208,24 @@ def test_a_workspace_of_another_call_serves(m, kernel, cdt):
         check(c, d, rows={(0, 0), (0, n - 1)})
 
 
+def test_zero_scale_behind_a_half_that_is_not_there(m, kernel):
+    """The window starts in the middle of a 32-key chunk, whose first 16 keys come in as zeros with their scales; the next
+    page that the same warp reads (80 users: a CTA a tile, a chunk in four a warp) has a scale of zero itself, and the
+    largest scores."""
+    B, old = 80, 299 + 16 + 32 * 20  # the window's first key stands at 656 = 32 * 20 + 16
+    c = Case([1] * B, [old] * B, 2, 8, 64, 16, BF16, ao.E4M3, window=300)
+    c.vs[:] = 2.0 ** -30
+    c.vc = c.vc.float().abs().clamp(min=2.0 ** -6).to(ao.E4M3)
+    for b in range(B):
+        pg = int(c.table[b, 48])  # chunk 24, the fifth of the window's
+        c.vs[pg] = 0.0
+        c.ks[pg] *= 20.0
+    d = c.cuda()
+    call(m, c, d)
+    m.lsa_check_device()
+    check(c, d, rows={(b, 0) for b in range(0, B, 7)})
+
+
 @pytest.mark.parametrize("test", ["strided_queries_and_no_lse", "large_scores_and_scale", "rows_with_nothing_to_see",
                                   "bad_data_is_left_out_and_flagged", "zero_scales", "many_sequences", "negative_and_zero_scale",
                                   "replayed_graph_follows_the_lengths", "two_streams_with_their_own_workspaces",
